@@ -50,7 +50,9 @@ typedef enum hq_status {
     HQ_ERR_WORKSPACE = 4,   /* workspace missing or smaller than the query */
     HQ_ERR_UNSUPPORTED = 5, /* unknown flag, mode, layout or transform size */
     HQ_ERR_CUDA = 6,        /* the CUDA runtime reported an error */
-    HQ_ERR_TIMEOUT = 7      /* a bounded device-side wait gave up */
+    HQ_ERR_TIMEOUT = 7,     /* a bounded device-side wait gave up */
+    HQ_ERR_PAGE = 8         /* a block table or a length points outside the cache
+                               (device error word of hq_kv4_attention) */
 } hq_status;
 
 /* hq_group_rht_quant flags */
@@ -414,6 +416,268 @@ hq_status hq_convert(int fmt, const float *in, uint8_t *out, int64_t n, void *st
  * alignment.  Errors: HQ_ERR_NULL, HQ_ERR_SHAPE, HQ_ERR_CUDA.
  */
 hq_status hq_convert_e2m1_sr(const float *in, const uint8_t *rnd, uint8_t *out, int64_t n, void *stream);
+
+/* ======================================================================
+ * The attention layer around the quantizers: residual + RMS norm with FP8
+ * codes, rotary positions, slot maps, the NVFP4 key/value cache and
+ * attention over it.
+ *
+ * Common rules of these calls: element types are HQ_DT_*; strides are in
+ * elements; rows (the last dimension) are contiguous; tensors of one call are
+ * on the current device.  Checks come before any launch; nothing is allocated
+ * and nothing synchronizes.  Outputs must not overlap inputs except where a
+ * call says so.
+ * ====================================================================== */
+
+/* element types */
+#define HQ_DT_BF16 0
+#define HQ_DT_F16 1
+#define HQ_DT_F32 2
+
+#define HQ_NORM_MAX_K 65536
+
+/*
+ * Residual addition, root-mean-square norm and K128 FP8 codes in one pass over
+ * the rows (the activation quantizer's rule, hq_swiglu_fp8_k128, applied to
+ * the normalized row):
+ *   h = x + r rounded to the type (h = x without a residual),
+ *   rstd = 1 / sqrt(mean(h^2) + eps), y = (h * rstd) * w in FP32,
+ *   per group of 128 columns: s = max(amax, 1e-10) * float32(1/448),
+ *   code = E4M3(y / s).
+ *
+ *  dtype      type of x, residual and residual_out; w_dtype: dtype or HQ_DT_F32.
+ *  x, residual  [M, K], row strides given; residual NULL: none.
+ *  weight     [K].   eps  >= 0.
+ *  residual_out [M, K] contiguous: h (needed with a residual, else ignored).
+ *             May be x or residual itself where that is contiguous.
+ *  out_fp8    uint8 [M, K].
+ *  scales     float: HQ_SCALE_ROWMAJOR [M, K/128], or HQ_SCALE_TRANSPOSED
+ *             [K/128, scale_ld] (scale_ld >= M; columns behind M are left as
+ *             they were); either may add HQ_FP8_UE8M0.
+ *  rstd_opt   float [M] or NULL (the backward pass reads it).
+ *  amax_opt   float, the groups' max |y| in the scales' layout, or NULL.
+ *  K          multiple of 128, at most HQ_NORM_MAX_K.
+ * A row with a NaN or an infinity has codes that are NaN wherever y is; the
+ * group rule skips NaNs.  Squares are summed in FP32: |h| above 1e19 gives
+ * rstd = 0.
+ * Alignment: 16 bytes (rstd, scales, amax: 4), strides multiples of 8.
+ * Errors: HQ_ERR_NULL, HQ_ERR_SHAPE, HQ_ERR_ALIGN, HQ_ERR_UNSUPPORTED,
+ *         HQ_ERR_CUDA.
+ */
+hq_status hq_add_rmsnorm_fp8_k128(int dtype, const void *x, int64_t x_row_stride,
+                                  const void *residual, int64_t residual_row_stride,
+                                  const void *weight, int w_dtype, float eps, int64_t M, int64_t K,
+                                  void *residual_out, uint8_t *out_fp8, float *scales, int scale_layout,
+                                  int64_t scale_ld, float *rstd_opt, float *amax_opt, void *stream);
+
+/*
+ * The norm's gradients (the codes' rounding passes them straight through):
+ *   g = dy * w, c = rstd^2 * mean(g * h), dx = rstd * (g - h * c) + dres,
+ *   dweight = sum over the rows of dy * h * rstd.
+ * dx is the gradient of x and of the residual alike.
+ *  dtype      type of dy, h, dres and dx; w_dtype: dtype or HQ_DT_F32.
+ *  dy, h, dres  [M, K] with row strides (dres NULL: none); rstd float [M].
+ *  dx         [M, K] contiguous; may be dy or dres itself where contiguous.
+ *  dweight    float [K], or NULL.
+ *  ws         >= hq_rmsnorm_backward_workspace_size(M, K) bytes, 16-byte
+ *             aligned, any contents (unused without dweight: may be NULL).
+ * The sum over the rows is taken in a fixed order: equal inputs give equal
+ * bits on one GPU model.  M == 0 gives dweight = 0.
+ * Alignment and errors as above, and HQ_ERR_WORKSPACE.
+ */
+size_t hq_rmsnorm_backward_workspace_size(int64_t M, int64_t K);
+hq_status hq_rmsnorm_backward(int dtype, const void *dy, int64_t dy_row_stride, const void *h,
+                              int64_t h_row_stride, const void *weight, int w_dtype, const float *rstd,
+                              const void *dres, int64_t dres_row_stride, int64_t M, int64_t K, void *dx,
+                              float *dweight, void *ws, size_t ws_bytes, void *stream);
+
+/* hq_rope layouts: which two elements of the rotated part make pair i */
+#define HQ_ROPE_HALVES 0      /* i and i + rotary_dim / 2 */
+#define HQ_ROPE_INTERLEAVED 1 /* 2 i and 2 i + 1 */
+
+/* hq_rope_inv_freq scalings */
+#define HQ_ROPE_PLAIN 0  /* base^(-2 i / rotary_dim) */
+#define HQ_ROPE_LINEAR 1 /* divided by factor */
+#define HQ_ROPE_NTK 2    /* base * factor^(rotary_dim / (rotary_dim - 2)) */
+#define HQ_ROPE_PARTS 3  /* by parts: pairs that turn more than p1 times within
+                            trained_len keep their frequency, those below p2
+                            turns are divided by factor, a linear ramp over the
+                            pair index between (its ends rounded outwards);
+                            magnitude 0.1 ln(factor) + 1 */
+#define HQ_ROPE_BANDS 4  /* by wavelength L: L < trained_len / p2 keeps, L >
+                            trained_len / p1 is divided by factor, between the
+                            two are mixed linearly in trained_len / L (p2 > p1) */
+
+/*
+ * Rotary frequencies in radians per position, on the host, in FP64:
+ * inv_freq[rotary_dim / 2] and *magnitude (may be NULL), the factor that
+ * hq_rope multiplies both cosine and sine with.  factor >= 1; trained_len, p1,
+ * p2 (> 0) are read by HQ_ROPE_PARTS and HQ_ROPE_BANDS.
+ * Errors: HQ_ERR_NULL, HQ_ERR_SHAPE (rotary_dim odd or < 2; NTK: < 4),
+ *         HQ_ERR_UNSUPPORTED (unknown scaling, parameters out of range).
+ */
+hq_status hq_rope_inv_freq(int rotary_dim, double base, int scaling, double factor, double trained_len,
+                           double p1, double p2, double *inv_freq, double *magnitude);
+
+/*
+ * Rotary positions of q and k in one launch: dimensions [offset, offset +
+ * rotary_dim) of each head are turned pair by pair by the angle
+ * position * inv_freq[i]; the others are passed through.
+ *   (a, b) -> m (a cos - b sin), m (a sin + b cos), FP32, rounded once.
+ * inverse != 0 turns by minus the angle (the gradient: the transpose of the
+ * rotation, times the same magnitude).
+ *  q, k       [T, Hq, D], [T, Hk, D]; strides of token and head; k may be NULL
+ *             (Hk == 0).
+ *  positions  int64 [T], any value (angles are reduced in FP64: absolute error
+ *             below 4e-7 + |position| * inv_freq * 2^-50 radians).
+ *  inv_freq   device double [rotary_dim / 2].
+ *  q_out, k_out  same shapes, own strides; may be q and k themselves (same
+ *             strides).
+ * Any D, rotary_dim (even), offset and strides; 16-byte aligned rows with
+ * whole chunks of 8 elements take wide loads, others element by element.
+ * Alignment: to the element (positions, inv_freq 8 bytes).
+ * Errors: HQ_ERR_NULL, HQ_ERR_SHAPE, HQ_ERR_ALIGN, HQ_ERR_UNSUPPORTED,
+ *         HQ_ERR_CUDA.
+ */
+hq_status hq_rope(int dtype, const void *q, int64_t q_token_stride, int64_t q_head_stride, int Hq,
+                  const void *k, int64_t k_token_stride, int64_t k_head_stride, int Hk, int64_t T, int D,
+                  const int64_t *positions, const double *inv_freq, int rotary_dim, int offset, int layout,
+                  float magnitude, int inverse, void *q_out, int64_t q_out_token_stride,
+                  int64_t q_out_head_stride, void *k_out, int64_t k_out_token_stride,
+                  int64_t k_out_head_stride, void *stream);
+
+/*
+ * Block tables and slot maps of one step, on the GPU.  Pages of page_size
+ * tokens are held by requests (block_table) or lie on a stack (free_pages,
+ * its height *free_count).
+ *  lens        int32 [B], tokens cached so far.
+ *  new_tokens  int32 [B], tokens to come in this step; < 0: the request has
+ *              ended.
+ *  block_table int32 [B, table_width], row stride table_width; entries below
+ *              ceil(lens / page_size) are the request's pages.
+ * In this order: the pages of ended requests go onto the stack (by request,
+ * then page); the pages that the others need for lens + new_tokens come off
+ * its top (by request, then page) into their rows.
+ *  lens_out    int32 [B]: lens + new_tokens, 0 for ended requests.
+ *  cu_new      int32 [B + 1]: running sum of the new tokens (0 where ended).
+ *  slots, positions  int64 [n_slots]: for new token j of request b at row
+ *              cu_new[b] + j its place in the cache, page * page_size +
+ *              position % page_size, and its position lens[b] + j.  Rows
+ *              behind the last token: slot -1, position 0.
+ *  free_count_out  int32 [1].
+ *  status      int32 [1]: 0, or a sum of HQ_KV_* reasons.  Then nothing is
+ *              taken or given back: lens_out = lens, *free_count_out =
+ *              *free_count, cu_new and positions 0, slots -1, block_table and
+ *              free_pages unchanged.
+ * lens_out may be lens, free_count_out may be free_count.  B <=
+ * HQ_KV_MAX_REQUESTS; page_size a power of two from 16 to 1024.
+ * Errors: HQ_ERR_NULL, HQ_ERR_SHAPE, HQ_ERR_ALIGN, HQ_ERR_UNSUPPORTED
+ *         (page_size), HQ_ERR_CUDA.
+ */
+#define HQ_KV_MAX_REQUESTS 4096
+#define HQ_KV_NO_PAGES 1   /* fewer free pages than the step needs */
+#define HQ_KV_NO_ROWS 2    /* more new tokens than n_slots */
+#define HQ_KV_NO_WIDTH 4   /* a request outgrows its row of the block table */
+#define HQ_KV_BAD_STATE 8  /* a length is negative or does not fit its row, the stack's height is
+                              outside [0, free_capacity], or its pages would not fit */
+hq_status hq_kv_slots(int B, const int32_t *lens, const int32_t *new_tokens, int32_t *block_table,
+                      int64_t table_width, int32_t *free_pages, int64_t free_capacity,
+                      const int32_t *free_count, int page_size, int64_t n_slots, int32_t *lens_out,
+                      int32_t *cu_new, int64_t *slots, int64_t *positions, int32_t *free_count_out,
+                      int32_t *status, void *stream);
+
+/*
+ * The NVFP4 key/value cache: uint8 [num_pages, H, page_size / 16, 2432].  Keys
+ * and values of HQ_KV4_HEAD = 128 dimensions are quantized one 128-vector at a
+ * time as by hq_cat_rotate_nvfp4 (after the same 128-point Hadamard rotation
+ * when hadamard_n is 128), 64 + 8 + 4 bytes each.  A group of 16 tokens of one
+ * head holds, in bytes (token r, 16-element block b, element d = 16 b + e):
+ *      0  K codes, pair (d, d + 1), e = 4 i + 2 j, i < 4, j < 2:
+ *         64 r + 16 i + 2 b + j
+ *   1024  V codes, pair (d, d + 1), e = 2 g, g < 8:
+ *         512 (r / 8) + 64 g + 16 (r % 8 / 2) + 8 (r % 2) + b
+ *   2048  K block scales (E4M3): 8 r + b
+ *   2176  V block scales: 64 (r / 8) + 16 (r % 8 / 2) + 2 b + r % 2
+ *   2304  K decode scales (float): 4 r
+ *   2368  V decode scales (float): 4 r
+ * so that a group is one contiguous copy and a lane of the attention kernel
+ * finds the operands of its matrix instructions in 16-byte pieces.
+ * Slot s is token s % page_size of page s / page_size.
+ * page_size: a power of two from 16 to 1024.
+ */
+#define HQ_KV4_HEAD 128
+#define HQ_KV4_GROUP_TOKENS 16
+#define HQ_KV4_GROUP_BYTES 2432
+/* bytes of a cache; 0 for sizes out of range */
+size_t hq_kv4_cache_bytes(int64_t num_pages, int page_size, int H);
+
+/*
+ * Quantize new keys and values into the cache.
+ *  k, v       [N, H, 128], strides of token and head, dtype HQ_DT_*.
+ *  slots      int64 [N]; a slot outside [0, num_pages * page_size) is skipped
+ *             (padding rows).  Slots of one call must differ: of a slot given
+ *             twice the contents are undefined (no other slot is touched).
+ *  hadamard_n 128 or 0.
+ * Values must be finite.  Alignment: k, v 16 bytes, strides multiples of 8,
+ * cache 16 bytes, slots 8.
+ * Errors: HQ_ERR_NULL, HQ_ERR_SHAPE, HQ_ERR_ALIGN, HQ_ERR_UNSUPPORTED,
+ *         HQ_ERR_CUDA.
+ */
+hq_status hq_kv4_append(int dtype, const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                        int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots, int64_t N, int H,
+                        int hadamard_n, uint8_t *cache, int64_t num_pages, int page_size, void *stream);
+
+/*
+ * Read tokens back: k_out, v_out [N, H, 128] in dtype, each value code * block
+ * scale * decode scale in FP32, rotated back (hadamard_n 128) or as stored (0),
+ * rounded once.  A slot outside the cache gives zeros.  A slot may be given
+ * more than once.  Other arguments and errors as hq_kv4_append.
+ */
+hq_status hq_kv4_gather(int dtype, const uint8_t *cache, int64_t num_pages, int page_size, const int64_t *slots,
+                        int64_t N, int H, int hadamard_n, void *k_out, int64_t k_token_stride,
+                        int64_t k_head_stride, void *v_out, int64_t v_token_stride, int64_t v_head_stride,
+                        void *stream);
+
+/*
+ * Attention of the newest tokens of each request over the cache (their own
+ * keys and values already appended).
+ *  q, out     [Tq, Hq, 128], strides of token and head, dtype HQ_DT_BF16 or
+ *             HQ_DT_F16.  Query head h reads key/value head h / (Hq / Hkv).
+ *  block_table int32 [B, table_width], seq_lens int32 [B]: tokens in the cache,
+ *             the queries' own among them.
+ *  cu_q       int32 [B + 1] or NULL: request b's queries are rows [cu_q[b],
+ *             cu_q[b + 1]), at most q_len of them; NULL: rows [b q_len,
+ *             (b + 1) q_len).  Query j of n is at position seq_len - n + j.
+ *  A query at position p sees the tokens t <= p, and with window > 0 only those
+ *  with p - t < window or t < sinks.
+ *   s_t = scale * q . k_t, out = sum_t softmax(s)_t v_t, lse = ln sum_t exp s_t
+ *  over the tokens it sees; none: out = 0, lse = -inf.
+ *  hadamard_n the one that the cache was written with: q is rotated before,
+ *             out rotated back after (rotations keep q . k).
+ *  lse_opt    float [Tq, Hq] or NULL.
+ *  Rows of out and lse behind the last request's are left as they were.
+ *  ws         >= hq_kv4_attention_workspace_size() bytes, 16-byte aligned, in
+ *             the rest state (hq_workspace_init); the call leaves it so.  Calls
+ *             that share one must not overlap in time.
+ * A block-table entry outside [0, num_pages) or a seq_len beyond the row's
+ * table_width * page_size tokens sets the workspace's error word to HQ_ERR_PAGE
+ * (hq_get_error); the tokens without a page count as not seen.
+ * Arithmetic: scores in FP32 from FP16 keys (exact) and a two-part FP16 query,
+ * weights rounded to FP16 for the second product, sums in FP32.  Results do not
+ * depend on anything but the inputs and the GPU's SM count.
+ * Alignment: q, out, cache, ws 16 bytes, strides of q and out multiples of 8.
+ * Errors: HQ_ERR_NULL, HQ_ERR_SHAPE (B > HQ_KV_MAX_REQUESTS, Hq not a multiple
+ *         of Hkv, q_len * Hq / Hkv > 65536), HQ_ERR_ALIGN, HQ_ERR_WORKSPACE,
+ *         HQ_ERR_UNSUPPORTED (dtype, hadamard_n, page_size, a negative window),
+ *         HQ_ERR_CUDA.
+ */
+size_t hq_kv4_attention_workspace_size(void);
+hq_status hq_kv4_attention(int dtype, const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t Tq,
+                           int Hq, const uint8_t *cache, int64_t num_pages, int page_size, int Hkv,
+                           const int32_t *block_table, int64_t table_width, int B, const int32_t *seq_lens,
+                           const int32_t *cu_q, int q_len, float scale, int window, int sinks, int hadamard_n,
+                           void *out, int64_t out_token_stride, int64_t out_head_stride, float *lse_opt,
+                           void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -4,7 +4,8 @@ Every function below passes raw device pointers and sizes to the compiled
 library ``libhq.so`` (CUDA kernels for sm_100a); no step of the computation
 runs in Python or PyTorch.  PyTorch is used for device memory and streams.
 If the library is missing or fails to load, importing the compute functions
-raises: there is no fallback.
+raises: there is no fallback.  ``layer.py`` holds the calls of the attention
+layer around the quantizers; all names are reached from the package itself.
 
 Low-level calls (``hq_*``) take caller-allocated output tensors exactly like
 the C functions.  ``group_rht_quant``, ``cat_rotate_fp8`` and
@@ -21,7 +22,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libhq.so")
 
 HQ_OK, HQ_ERR_NULL, HQ_ERR_SHAPE, HQ_ERR_ALIGN, HQ_ERR_WORKSPACE, HQ_ERR_UNSUPPORTED, HQ_ERR_CUDA, \
-    HQ_ERR_TIMEOUT = range(8)
+    HQ_ERR_TIMEOUT, HQ_ERR_PAGE = range(9)
 HQ_ROWWISE, HQ_COLWISE, HQ_ROW_RHT, HQ_TWO_PASS, HQ_AMAX_GIVEN, HQ_ROW_SR, HQ_COL_SR = 1, 2, 4, 8, 16, 32, 64
 HQ_SCALE_ROWMAJOR, HQ_SCALE_TRANSPOSED = 0, 1
 HQ_SF_SWIZZLED, HQ_FP8_UE8M0 = 128, 256  # scale formats (see include/hq.h)
@@ -36,6 +37,9 @@ EXPORTED = (
     "hq_group_rht_quant_host", "hq_group_rht_quant_host_device_bytes", "hq_cat_rotate_fp8",
     "hq_cat_rotate_fp8_workspace_size", "hq_cat_rotate_nvfp4", "hq_cat_rotate_nvfp4_workspace_size",
     "hq_swiglu_fp8_k128", "hq_swiglu_fp8_k128_workspace_size", "hq_convert", "hq_convert_e2m1_sr",
+    "hq_add_rmsnorm_fp8_k128", "hq_rmsnorm_backward_workspace_size", "hq_rmsnorm_backward", "hq_rope_inv_freq", "hq_rope",
+    "hq_kv_slots", "hq_kv4_cache_bytes", "hq_kv4_append", "hq_kv4_gather", "hq_kv4_attention_workspace_size",
+    "hq_kv4_attention",
 )
 
 
@@ -99,6 +103,9 @@ def lib() -> ctypes.CDLL:
         L.hq_convert.argtypes = [c_int, P, P, i64, P]
         L.hq_convert_e2m1_sr.restype = c_int
         L.hq_convert_e2m1_sr.argtypes = [P, P, P, i64, P]
+        for name, (result, arguments) in layer.SIGNATURES.items():
+            f = getattr(L, name)
+            f.restype, f.argtypes = result, arguments
         _lib = L
     return _lib
 
@@ -390,3 +397,8 @@ def swiglu_fp8_k128(mode: int, inp: torch.Tensor, K_out: int, want_amax: bool = 
     amax = torch.empty_like(scales) if want_amax else None
     hq_swiglu_fp8_k128(mode, inp, M, K_out, codes, scales, amax, stream)
     return (codes, scales, amax) if want_amax else (codes, scales)
+
+
+# the attention layer around the quantizers (bindings and conveniences of its calls)
+from . import layer  # noqa: E402
+from .layer import *  # noqa: E402,F401,F403

@@ -148,6 +148,7 @@ const char* hq_status_string(hq_status s) {
         case HQ_ERR_UNSUPPORTED: return "unsupported flag, mode, layout or transform size";
         case HQ_ERR_CUDA: return "CUDA runtime error";
         case HQ_ERR_TIMEOUT: return "bounded device wait gave up";
+        case HQ_ERR_PAGE: return "block table or length points outside the cache";
     }
     return "unknown status";
 }
