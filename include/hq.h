@@ -667,7 +667,8 @@ hq_status hq_kv4_gather(int dtype, const uint8_t *cache, int64_t num_pages, int 
  * depend on anything but the inputs and the GPU's SM count.
  * Alignment: q, out, cache, ws 16 bytes, strides of q and out multiples of 8.
  * Errors: HQ_ERR_NULL, HQ_ERR_SHAPE (B > HQ_KV_MAX_REQUESTS, Hq not a multiple
- *         of Hkv, q_len * Hq / Hkv > 65536), HQ_ERR_ALIGN, HQ_ERR_WORKSPACE,
+ *         of Hkv, q_len * Hq / Hkv > 65536, a table row of more than 2^30
+ *         tokens), HQ_ERR_ALIGN, HQ_ERR_WORKSPACE,
  *         HQ_ERR_UNSUPPORTED (dtype, hadamard_n, page_size, a negative window),
  *         HQ_ERR_CUDA.
  */

@@ -1,151 +1,666 @@
 // hq_attn.cu -- attention of the newest tokens over the NVFP4 cache (sm_100a).
+//
+// For the columns n of one (request, key/value head) -- a column is one query
+// head of one query token, NC = 8 or 16 of them at a time -- and its tokens t
+//   s_tn = scale * q_n . k_t,  o_n = sum_t exp(s_tn - m_n) v_t,  l_n = sum_t exp(s_tn - m_n).
+// A warp takes groups of 16 tokens.  Both products are m16n8k16 matrix
+// instructions with the columns as their n side, so that 8 query heads of one
+// key/value head fill them:
+//   S^T [16 tokens, n] = K [16, 128] q^T     (8 instructions a part of q)
+//   O^T [16 d,      n] += V^T [16 d, 16 t] P^T  (8 instructions, one per 16-element block)
+// A block scale covers exactly one instruction's depth (K) or height (V):
+//  * K codes are widened to FP16 (exact) and multiplied unscaled; each block's
+//    FP32 product is scaled by its token's E4M3 block scale as it is added up.
+//    q is split into two FP16 parts (hi + lo, 22 bits), so scores are FP32-like.
+//  * for V the weights are scaled instead: P (FP16) times the tokens' block
+//    scales of that block, half as many multiplications as V's codes.
+// The cache's byte order gives each lane its operands of a group as 16-byte
+// pieces (four for the codes, three for the block scales).
+//
+// The running maximum moves only when a score exceeds it by 5 (in powers of
+// two), so the usual group needs no exchange between lanes: weights stay at
+// or below 32, and the decode scales of V, taken relative to the largest seen
+// so far, at or below 1; 32 * 448 is inside FP16.
 #include "hq_layer.cuh"
 
 namespace hq {
 
-constexpr int ATTN_COLS = 8, ATTN_WARPS = 4;
+#ifndef HQ_ATTN_STAGES
+#define HQ_ATTN_STAGES 3
+#endif
+constexpr int ATTN_STAGES = HQ_ATTN_STAGES;       // groups in flight per warp
+constexpr int ATTN_MAX_CTAS = 1024;  // workspace: CTAs of a launch at most
+constexpr int ATTN_MAX_NC = 16;
+constexpr int ATTN_PART = ATTN_MAX_NC * (128 + 2);  // floats of one partial result
+constexpr float ATTN_NONE = -1e30f;  // running maximum before any token
 
-__device__ __forceinline__ float e2m1_value4(uint32_t c) {
-    const uint32_t m = c & 7u;
-    const float v = m < 2u ? 0.5f * (float)m : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
-    return c & 8u ? -v : v;
+// ---------------------------------------------------------------- schedule
+// Units are groups of 16 tokens, numbered request by request, then (head,
+// column tile) row by row, then group by group.  CTA c of G takes units
+// [U c / G, U (c + 1) / G): the same load for every CTA whatever the lengths.
+struct Request {
+    int q0, nq;       // first row of q, query tokens
+    int len;          // tokens (clamped to the block table's row)
+    int last;         // position of the last query
+    int tiles;        // column tiles
+    int sink_groups;  // groups of the first tokens, before the window's
+    int first_group;  // the window's first group
+    int n;            // groups per row (at least 1 where there are queries)
+    bool bad;         // the length exceeds the block table's row
+};
+
+__device__ __forceinline__ Request attn_request(const AttnParams& p, int b, int nc) {
+    Request r;
+    int64_t a = p.cu_q ? p.cu_q[b] : (int64_t)b * p.q_len, e = p.cu_q ? p.cu_q[b + 1] : a + p.q_len;
+    a = a < 0 ? 0 : a;
+    e = e > p.Tq ? p.Tq : e;
+    r.q0 = (int)a;
+    r.nq = (int)(e - a < 0 ? 0 : (e - a > p.q_len ? p.q_len : e - a));
+    const int64_t row = p.width << p.page_shift;
+    const int len = p.lens[b];
+    r.last = len - 1;
+    r.bad = len > row;
+    r.len = len < 0 ? 0 : (r.bad ? (int)row : len);
+    r.tiles = (r.nq * p.group + nc - 1) / nc;
+    // the window's first token (lengths are below 2^30: host check)
+    const int64_t first = (int64_t)r.last - r.nq + 1 - p.window + 1;
+    const int lo = p.window > 0 && first > 0 ? (int)min(first, (int64_t)r.len) : 0;
+    r.first_group = lo >> 4;
+    r.sink_groups = min((min(p.sinks, lo) + 15) >> 4, r.first_group);
+    r.n = r.nq ? max(1, r.sink_groups + ((r.len + 15) >> 4) - r.first_group) : 0;
+    return r;
 }
 
-// Unnormalised 128-point butterfly over a warp, lane l with elements 4 l ..
-// 4 l + 3, and the factor 1 / sqrt(128).
+// A CTA's walk over its pieces: a piece is a run of groups of one row.
+struct Walk {
+    Request r;
+    int b, row;           // request, row (head, column tile) of it
+    int ja, jb;           // groups of the piece: [ja, jb) of r.n
+    uint64_t at, end;     // next unit, end of the CTA's units
+    bool live;
+};
+
+struct Sched {
+    uint64_t U;
+    uint32_t G;
+};
+
+__device__ __forceinline__ uint64_t cta_first(const Sched& s, uint32_t c) { return s.U * c / s.G; }
+// The CTA that holds unit u.
+__device__ __forceinline__ uint32_t cta_of(const Sched& s, uint64_t u) { return (uint32_t)(((u + 1) * s.G - 1) / s.U); }
+
+__device__ __forceinline__ void walk_piece(const AttnParams& p, const uint64_t* pre, int nc, Walk& w) {
+    w.live = w.at < w.end;
+    if (!w.live) return;
+    const uint64_t in = w.at - pre[w.b];
+    w.row = (int)(in / (uint32_t)w.r.n);
+    w.ja = (int)(in - (uint64_t)w.row * w.r.n);
+    const uint64_t left = w.end - w.at;
+    w.jb = left < (uint64_t)(w.r.n - w.ja) ? w.ja + (int)left : w.r.n;
+}
+__device__ __forceinline__ void walk_start(const AttnParams& p, const uint64_t* pre, int nc, uint64_t at, uint64_t end,
+                                           Walk& w) {
+    w.at = at;
+    w.end = end;
+    w.live = at < end;
+    if (!w.live) return;
+    int lo = 0, hi = p.B - 1;  // the request with pre[b] <= at < pre[b + 1]
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid + 1] > at) hi = mid;
+        else lo = mid + 1;
+    }
+    w.b = lo;
+    w.r = attn_request(p, lo, nc);
+    walk_piece(p, pre, nc, w);
+}
+__device__ __forceinline__ void walk_next(const AttnParams& p, const uint64_t* pre, int nc, Walk& w) {
+    w.at += (uint64_t)(w.jb - w.ja);
+    if (w.at < w.end && w.at >= pre[w.b + 1]) {
+        do ++w.b;
+        while (w.at >= pre[w.b + 1]);
+        w.r = attn_request(p, w.b, nc);
+    }
+    walk_piece(p, pre, nc, w);
+}
+
+// ------------------------------------------------------------------ device
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Four bytes of E2M1 pairs -> four FP16 pairs (low nibble in the low half).
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+// Two pairs of E4M3 bytes -> two FP16 pairs (exact).
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float2 h2f(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect(uint64_t* bar, uint32_t bytes) {
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}"
+                 :: "r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+// 128-point butterfly over a warp, lane l with elements 4 l .. 4 l + 3, and
+// the factor 1 / sqrt(128).
 __device__ __forceinline__ void rotate_warp(float (&y)[4], int lane) {
-    const float a = y[0] + y[1], b = y[0] - y[1], c = y[2] + y[3], d = y[2] - y[3];
-    y[0] = a + c;
-    y[1] = b + d;
-    y[2] = a - c;
-    y[3] = b - d;
+    const float a = __fadd_rn(y[0], y[1]), b = __fsub_rn(y[0], y[1]), c = __fadd_rn(y[2], y[3]), d = __fsub_rn(y[2], y[3]);
+    y[0] = __fadd_rn(a, c);
+    y[1] = __fadd_rn(b, d);
+    y[2] = __fsub_rn(a, c);
+    y[3] = __fsub_rn(b, d);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float other = __shfl_xor_sync(0xFFFFFFFFu, y[i], o);
-            y[i] = lane & o ? other - y[i] : y[i] + other;
+            y[i] = lane & o ? __fsub_rn(other, y[i]) : __fadd_rn(y[i], other);
         }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] *= 0.08838834764831845f;
+    for (int i = 0; i < 4; ++i) y[i] = __fmul_rn(y[i], 0.08838834764831845f);
 }
 
-// One block per (request, key/value head, 8 columns); a column is one query
-// head of one query token.  A warp takes every fourth token, a lane four
-// dimensions of it.
-template <int DT> __global__ void __launch_bounds__(32 * ATTN_WARPS) kv4_attention_kernel(AttnParams p) {
+// Shared memory of a CTA of W warps with NC columns.
+template <int NT, int W> struct AttnShared {
+    static constexpr int NC = 8 * NT, OS = 132;  // columns; padded row of the merge buffer (free of bank conflicts)
+    alignas(128) uint8_t ring[W][ATTN_STAGES][KV_GROUP_BYTES];
+    float o[W][NC][OS];
+    uint32_t q[2][NC][64];  // hi and lo parts, FP16 pairs
+    float m[W][NC], l[W][NC];
+    float qs[NC];  // factor of a column's scores, in powers of two
+    uint64_t full[W][ATTN_STAGES];
+    unsigned long long warp_sums[W];
+    int last;
+    // then the units before each request, uint64_t [B + 1]
+};
+
+template <int DT, int NT, int W, int MINB>
+__global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams p) {
     typedef typename Elem<DT>::T T;
-    __shared__ float so[ATTN_WARPS][ATTN_COLS][128], sm[ATTN_WARPS][ATTN_COLS], sl[ATTN_WARPS][ATTN_COLS];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, quad = lane & 3, blk = lane >> 2;
-    const int b = blockIdx.x, kvh = blockIdx.y, col0 = blockIdx.z * ATTN_COLS;
-    int64_t q0 = p.cu_q ? p.cu_q[b] : (int64_t)b * p.q_len, q1 = p.cu_q ? p.cu_q[b + 1] : q0 + p.q_len;
-    if (q0 < 0) q0 = 0;
-    if (q1 > p.Tq) q1 = p.Tq;
-    const int nq = (int)(q1 - q0 < 0 ? 0 : (q1 - q0 > p.q_len ? p.q_len : q1 - q0)), cols = nq * p.group;
-    if (col0 >= cols) return;
-    const int64_t row_tokens = p.width << p.page_shift;
-    int len = p.lens[b];
+    typedef AttnShared<NT, W> Shared;
+    constexpr int NC = 8 * NT, S = ATTN_STAGES;
+    extern __shared__ __align__(128) uint8_t raw[];
+    Shared& sh = *reinterpret_cast<Shared*>(raw);
+    uint64_t* const pre = reinterpret_cast<uint64_t*>(raw + sizeof(Shared));
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, i4 = lane & 3;
+
+    if (lane < S) mbar_init(&sh.full[w][lane], 1);
+    // ---- units before each request
+    unsigned long long carry = 0;
     bool bad = false;
-    if (len > row_tokens) {
-        bad = true;
-        len = (int)row_tokens;
+    for (int b0 = 0; b0 < p.B; b0 += 32 * W) {
+        const int b = b0 + tid;
+        unsigned long long v = 0;
+        if (b < p.B) {
+            const Request r = attn_request(p, b, NC);
+            v = (unsigned long long)r.tiles * p.Hkv * r.n;
+            bad |= r.bad && r.nq;
+        }
+        unsigned long long s = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+            if (lane >= o) s += u;
+        }
+        if (lane == 31) sh.warp_sums[w] = s;
+        __syncthreads();
+        unsigned long long before = carry, total = 0;
+        for (int k = 0; k < W; ++k) {
+            if (k < w) before += sh.warp_sums[k];
+            total += sh.warp_sums[k];
+        }
+        if (b < p.B) pre[b] = before + s - v;
+        carry += total;
+        __syncthreads();
     }
-    const int pos_last = p.lens[b] - 1;
-    const int groups = 1 << (p.page_shift - 4);
-    float q[ATTN_COLS][4], o[ATTN_COLS][4] = {}, m[ATTN_COLS], l[ATTN_COLS] = {};
-    int pos[ATTN_COLS];
-#pragma unroll
-    for (int c = 0; c < ATTN_COLS; ++c) {
-        const int col = col0 + c;
-        m[c] = -INFINITY;
-        pos[c] = -1;
-        if (col < cols) {
-            const int j = col / p.group;
-            const T* x = static_cast<const T*>(p.q) + (q0 + j) * p.q_ts + (kvh * p.group + col % p.group) * p.q_hs;
-            pos[c] = pos_last - (nq - 1 - j);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) q[c][e] = to_f32(x[4 * lane + e]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) q[c][e] = 0.0f;
-        }
-        if (p.rotate) rotate_warp(q[c], lane);
-    }
-    for (int t = w; t < len; t += ATTN_WARPS) {
-        const int page = p.table[b * p.width + (t >> p.page_shift)];
-        if (page < 0 || page >= p.num_pages) {
-            bad = true;
-            continue;
-        }
-        const uint8_t* g = p.cache + (((int64_t)page * p.Hkv + kvh) * groups + ((t & ((1 << p.page_shift) - 1)) >> 4)) * KV_GROUP_BYTES;
-        const int r = t & 15, half = r >> 3, pair = (r & 7) >> 1, odd = r & 1;
-        const uint32_t kc = *reinterpret_cast<const uint16_t*>(g + KV_K_CODES + r * 64 + quad * 16 + blk * 2);
-        const float ks = e4m3_value(g[KV_K_SF + r * 8 + blk]) * reinterpret_cast<const float*>(g + KV_K_DEC)[r];
-        const uint8_t* vo = g + KV_V_CODES + half * 512 + pair * 16 + odd * 8 + blk;
-        const uint32_t vc = vo[(2 * quad) * 64] | (uint32_t)vo[(2 * quad + 1) * 64] << 8;
-        const float vs = e4m3_value(g[KV_V_SF + half * 64 + pair * 16 + blk * 2 + odd]) * reinterpret_cast<const float*>(g + KV_V_DEC)[r];
-        float k[4], v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            k[e] = e2m1_value4(kc >> (4 * e)) * ks;
-            v[e] = e2m1_value4(vc >> (4 * e)) * vs;
-        }
-#pragma unroll
-        for (int c = 0; c < ATTN_COLS; ++c) {
-            float s = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s = __fmaf_rn(q[c][e], k[e], s);
-            s = warp_sum(s) * p.scale;
-            const bool see = t <= pos[c] && (p.window == 0 || pos[c] - t < p.window || t < p.sinks);
-            if (!see) continue;
-            const float mn = fmaxf(m[c], s), a = expf(m[c] - mn), e = expf(s - mn);
-            m[c] = mn;
-            l[c] = l[c] * a + e;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[c][i] = __fmaf_rn(o[c][i], a, e * v[i]);
-        }
-    }
-    if (bad && lane == 0) p.ws[2] = HQ_ERR_PAGE;
-#pragma unroll
-    for (int c = 0; c < ATTN_COLS; ++c) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) so[w][c][4 * lane + i] = o[c][i];
-        if (lane == 0) {
-            sm[w][c] = m[c];
-            sl[w][c] = l[c];
-        }
-    }
+    if (tid == 0) pre[p.B] = carry;
+    fence_mbar_init();
     __syncthreads();
-    for (int c = w; c < ATTN_COLS; c += ATTN_WARPS) {
-        const int col = col0 + c;
-        if (col >= cols) continue;
-        float mx = -INFINITY, total = 0.0f, y[4] = {};
-        for (int i = 0; i < ATTN_WARPS; ++i) mx = fmaxf(mx, sm[i][c]);
-        for (int i = 0; i < ATTN_WARPS; ++i) {
-            if (sl[i][c] == 0.0f) continue;
-            const float a = expf(sm[i][c] - mx);
-            total += sl[i][c] * a;
-            for (int e = 0; e < 4; ++e) y[e] += so[i][c][4 * lane + e] * a;
+    Sched sc;
+    sc.U = carry;
+    if (sc.U == 0) return;
+    {  // at least one group per warp of a CTA
+        const uint64_t most = (sc.U + W - 1) / W;
+        sc.G = most < gridDim.x ? (uint32_t)most : gridDim.x;
+    }
+    if (blockIdx.x >= sc.G) return;
+    if (bad) p.ws[2] = HQ_ERR_PAGE;  // (every CTA that is not idle reports the same)
+
+    // ---- the warp's loads run ahead of its arithmetic, across pieces
+    Walk lw, cw;
+    walk_start(p, pre, NC, cta_first(sc, blockIdx.x), cta_first(sc, blockIdx.x + 1), cw);
+    lw = cw;
+    int lj = lw.ja + w;       // next group to load of lw's piece
+    int page = -1;            // its page (prefetched), or -1
+    uint32_t stage_ok = 0;    // bit s: stage s holds a group
+    const int groups_shift = p.page_shift - 4;
+    const uint32_t ring0 = smem_u32(sh.ring[w][0]);
+    auto group_of = [&](const Walk& k, int j) { return j < k.r.sink_groups ? j : k.r.first_group + (j - k.r.sink_groups); };
+    auto settle = [&]() {  // move to the next piece with a group for this warp
+        while (lw.live && lj >= lw.jb) {
+            walk_next(p, pre, NC, lw);
+            lj = lw.ja + w;
         }
-        for (int e = 0; e < 4; ++e) y[e] = total > 0.0f ? y[e] / total : 0.0f;
-        if (p.rotate) rotate_warp(y, lane);
-        const int j = col / p.group, head = kvh * p.group + col % p.group;
-        T* out = static_cast<T*>(p.out) + (q0 + j) * p.o_ts + head * p.o_hs;
-        for (int e = 0; e < 4; ++e) out[4 * lane + e] = from_f32<DT>(y[e]);
-        if (p.lse && lane == 0)
-            p.lse[(q0 + j) * (int64_t)(p.Hkv * p.group) + head] = total > 0.0f ? mx + logf(total) : -INFINITY;
+    };
+    auto fetch_page = [&]() {
+        page = -1;
+        if (lw.live) {
+            const int grp = group_of(lw, lj);
+            if (grp * 16 < lw.r.len) {
+                page = p.table[(int64_t)lw.b * p.width + (grp >> groups_shift)];
+                if (page < 0 || page >= p.num_pages) {
+                    page = -1;
+                    p.ws[2] = HQ_ERR_PAGE;
+                }
+            }
+        }
+    };
+    auto issue = [&](int st) {  // load the group at (lw, lj) into stage st, then look up the next one's page
+        stage_ok &= ~(1u << st);
+        if (!lw.live) return;
+        if (page >= 0) {
+            const int grp = group_of(lw, lj), head = lw.row / lw.r.tiles;
+            const uint8_t* src = p.cache + ((((int64_t)page * p.Hkv + head) << groups_shift) +
+                                            (grp & ((1 << groups_shift) - 1))) * KV_GROUP_BYTES;
+            if (lane == 0) {
+                mbar_arrive_expect(&sh.full[w][st], KV_GROUP_BYTES);
+                bulk_load(ring0 + st * KV_GROUP_BYTES, src, KV_GROUP_BYTES, &sh.full[w][st]);
+            }
+            stage_ok |= 1u << st;
+        }
+        lj += W;
+        settle();
+        fetch_page();
+    };
+    settle();
+    fetch_page();
+    for (int s = 0; s < S; ++s) issue(s);
+    int st = 0;
+    uint32_t phases = 0;  // bit s: parity of stage s's next completion
+
+    for (; cw.live; walk_next(p, pre, NC, cw)) {
+        const int head = cw.row / cw.r.tiles, col0 = (cw.row - head * cw.r.tiles) * NC, cols = cw.r.nq * p.group;
+        const int tile_cols = min(NC, cols - col0);
+        // ---- q: rotate, split into two FP16 parts, relative to the column's largest power of two
+        for (int c = w; c < NC; c += W) {
+            float y[4] = {};
+            if (c < tile_cols) {
+                const int j = (col0 + c) / p.group, hh = (col0 + c) - j * p.group;
+                const T* x = static_cast<const T*>(p.q) + (int64_t)(cw.r.q0 + j) * p.q_ts + (int64_t)(head * p.group + hh) * p.q_hs;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = to_f32(x[4 * lane + e]);
+            }
+            if (p.rotate) rotate_warp(y, lane);
+            float a = max3(fmaxf(fabsf(y[0]), fabsf(y[1])), fabsf(y[2]), fabsf(y[3]));
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+            // 2^e in (a / 2, a]; a zero, subnormal or infinite column keeps its values
+            const uint32_t ebits = __float_as_uint(a) & 0x7F800000u;
+            const bool plain = ebits < 0x08000000u || ebits > 0x77000000u;
+            const float up = plain ? 1.0f : __uint_as_float(ebits), down = plain ? 1.0f : __uint_as_float(0x7F000000u - ebits);
+            float hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float v = __fmul_rn(y[e], down);
+                hi[e] = __half2float(__float2half_rn(v));
+                lo[e] = __fsub_rn(v, hi[e]);
+            }
+            *reinterpret_cast<uint2*>(&sh.q[0][c][2 * lane]) = make_uint2(pack_h2(hi[0], hi[1]), pack_h2(hi[2], hi[3]));
+            *reinterpret_cast<uint2*>(&sh.q[1][c][2 * lane]) = make_uint2(pack_h2(lo[0], lo[1]), pack_h2(lo[2], lo[3]));
+            if (lane == 0) sh.qs[c] = up * p.scale * 1.4426950408889634f;
+        }
+        __syncthreads();
+        uint2 qf[2][NT][8];  // n side of the first product: column g, elements 16 b + 4 i .. + 3
+        float qs[NT][2];
+        int pos[NT][2], pos_min = 0x7FFFFFFF, pos_max = -1;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                qf[0][n][b] = *reinterpret_cast<const uint2*>(&sh.q[0][8 * n + g][8 * b + 2 * i4]);
+                qf[1][n][b] = *reinterpret_cast<const uint2*>(&sh.q[1][8 * n + g][8 * b + 2 * i4]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int c = 8 * n + 2 * i4 + k;
+                qs[n][k] = sh.qs[c];
+                pos[n][k] = cw.r.last - (cw.r.nq - 1 - min(col0 + c, cols - 1) / p.group);
+            }
+        }
+        pos_min = cw.r.last - (cw.r.nq - 1 - col0 / p.group);
+        pos_max = cw.r.last - (cw.r.nq - 1 - (col0 + tile_cols - 1) / p.group);
+
+        float o[NT][8][4], m[NT][2], l[NT][2], vmax = 0.0f, vinv = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][b][e] = 0.0f;
+            m[n][0] = m[n][1] = ATTN_NONE;
+            l[n][0] = l[n][1] = 0.0f;
+        }
+
+        for (int j = cw.ja + w; j < cw.jb; j += W) {
+            const int cur = st;
+            st = st + 1 == S ? 0 : st + 1;
+            if (!(stage_ok >> cur & 1u)) {  // no page: the tokens count as not seen
+                issue(cur);
+                continue;
+            }
+            // bounded by the copy's own end; a copy that never ends leaves the loop with an error (about 2 s)
+            bool got = mbar_try_wait_sleep(&sh.full[w][cur], phases >> cur & 1u, 1000000u);
+            for (int spin = 0; !got && spin < 2000; ++spin)
+                got = mbar_try_wait_sleep(&sh.full[w][cur], phases >> cur & 1u, 1000000u);
+            if (!got) p.ws[2] = HQ_ERR_TIMEOUT;
+            phases ^= 1u << cur;
+            const uint8_t* const grp = sh.ring[w][cur];
+            const int t0 = group_of(cw, j) * 16;
+
+            // ---- scores
+            float s[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
+            {
+                const uint4 k0 = *reinterpret_cast<const uint4*>(grp + KV_K_CODES + g * 64 + i4 * 16);
+                const uint4 k1 = *reinterpret_cast<const uint4*>(grp + KV_K_CODES + g * 64 + i4 * 16 + 512);
+                const uint2 f0 = *reinterpret_cast<const uint2*>(grp + KV_K_SF + g * 8);
+                const uint2 f1 = *reinterpret_cast<const uint2*>(grp + KV_K_SF + g * 8 + 64);
+                const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
+                uint32_t sf0[4], sf1[4];
+                e4m3x4_to_f16(f0.x, sf0[0], sf0[1]);
+                e4m3x4_to_f16(f0.y, sf0[2], sf0[3]);
+                e4m3x4_to_f16(f1.x, sf1[0], sf1[1]);
+                e4m3x4_to_f16(f1.y, sf1[2], sf1[3]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {  // blocks 2 q, 2 q + 1
+                    uint32_t a0[4], a1[4];
+                    e2m1x8_to_f16(kw0[q], a0);
+                    e2m1x8_to_f16(kw1[q], a1);
+                    const float2 x0 = h2f(sf0[q]), x1 = h2f(sf1[q]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint2 hi = qf[0][n][2 * q + k], lo = qf[1][n][2 * q + k];
+                            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                            mma16816(c, a0[2 * k], a1[2 * k], a0[2 * k + 1], a1[2 * k + 1], hi.x, hi.y);
+                            mma16816(c, a0[2 * k], a1[2 * k], a0[2 * k + 1], a1[2 * k + 1], lo.x, lo.y);
+                            const float y0 = k ? x0.y : x0.x, y1 = k ? x1.y : x1.x;
+                            s[n][0] = __fmaf_rn(y0, c[0], s[n][0]);
+                            s[n][1] = __fmaf_rn(y0, c[1], s[n][1]);
+                            s[n][2] = __fmaf_rn(y1, c[2], s[n][2]);
+                            s[n][3] = __fmaf_rn(y1, c[3], s[n][3]);
+                        }
+                    }
+                }
+                const float d0 = *reinterpret_cast<const float*>(grp + KV_K_DEC + 4 * g);
+                const float d1 = *reinterpret_cast<const float*>(grp + KV_K_DEC + 4 * g + 32);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    s[n][0] = __fmul_rn(s[n][0], __fmul_rn(d0, qs[n][0]));
+                    s[n][1] = __fmul_rn(s[n][1], __fmul_rn(d0, qs[n][1]));
+                    s[n][2] = __fmul_rn(s[n][2], __fmul_rn(d1, qs[n][0]));
+                    s[n][3] = __fmul_rn(s[n][3], __fmul_rn(d1, qs[n][1]));
+                }
+            }
+            float v0 = *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g);
+            float v1 = *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g + 32);
+            uint4 vf0 = *reinterpret_cast<const uint4*>(grp + KV_V_SF + i4 * 16);
+            uint4 vf1 = *reinterpret_cast<const uint4*>(grp + KV_V_SF + i4 * 16 + 64);
+            const bool whole = t0 + 15 <= pos_min && (p.window == 0 || pos_max - t0 < p.window || t0 + 15 < p.sinks);
+            if (!whole) {
+                const int ta = t0 + g, tb = ta + 8;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int q = pos[n][k];
+                        if (!(ta <= q && (p.window == 0 || q - ta < p.window || ta < p.sinks))) s[n][k] = -INFINITY;
+                        if (!(tb <= q && (p.window == 0 || q - tb < p.window || tb < p.sinks))) s[n][2 + k] = -INFINITY;
+                    }
+                // tokens behind the last query's position may hold anything: their value scales count as zero
+                if (ta > pos_max) v0 = 0.0f;
+                if (tb > pos_max) v1 = 0.0f;
+                const int e = pos_max - t0 - 2 * i4;  // the lane's even token is real if e >= 0, the odd one if e >= 1
+                const uint32_t keep0 = (e >= 0 ? 0x00FF00FFu : 0u) | (e >= 1 ? 0xFF00FF00u : 0u);
+                const uint32_t keep1 = (e >= 8 ? 0x00FF00FFu : 0u) | (e >= 9 ? 0xFF00FF00u : 0u);
+                vf0 = make_uint4(vf0.x & keep0, vf0.y & keep0, vf0.z & keep0, vf0.w & keep0);
+                vf1 = make_uint4(vf1.x & keep1, vf1.y & keep1, vf1.z & keep1, vf1.w & keep1);
+            }
+            // ---- move the references when a score or a value scale has outgrown them
+            bool grow = v0 * vinv > 1.0001f || v1 * vinv > 1.0001f || vmax == 0.0f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                grow |= fmaxf(s[n][0], s[n][2]) > m[n][0] + 5.0f || fmaxf(s[n][1], s[n][3]) > m[n][1] + 5.0f;
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+                float v = fmaxf(v0, v1);
+#pragma unroll
+                for (int x = 4; x <= 16; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, x));
+                v = fmaxf(v, vmax);
+                const float beta = v > 0.0f ? vmax / v : 0.0f;
+                vmax = v;
+                vinv = v > 0.0f ? 1.0f / v : 0.0f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float f[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float t = fmaxf(s[n][k], s[n][2 + k]);
+#pragma unroll
+                        for (int x = 4; x <= 16; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, x));
+                        t = fmaxf(t, m[n][k]);
+                        f[k] = ex2(m[n][k] - t);
+                        m[n][k] = t;
+                        l[n][k] *= f[k];
+                        f[k] *= beta;
+                    }
+#pragma unroll
+                    for (int b = 0; b < 8; ++b) {
+                        o[n][b][0] *= f[0];
+                        o[n][b][1] *= f[1];
+                        o[n][b][2] *= f[0];
+                        o[n][b][3] *= f[1];
+                    }
+                }
+            }
+            // ---- weights, as the n side of the second product
+            const float r0 = v0 * vinv, r1 = v1 * vinv;
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float e0 = ex2(s[n][0] - m[n][0]), e1 = ex2(s[n][1] - m[n][1]);
+                const float e2 = ex2(s[n][2] - m[n][0]), e3 = ex2(s[n][3] - m[n][1]);
+                l[n][0] += e0 + e2;
+                l[n][1] += e1 + e3;
+                pb[n][0] = transpose8x8(pack_h2(e0 * r0, e1 * r0));
+                pb[n][1] = transpose8x8(pack_h2(e2 * r1, e3 * r1));
+            }
+            // ---- values
+            const uint4 c0 = *reinterpret_cast<const uint4*>(grp + KV_V_CODES + lane * 16);
+            const uint4 c1 = *reinterpret_cast<const uint4*>(grp + KV_V_CODES + lane * 16 + 512);
+            const uint32_t ev0[2] = {c0.x, c0.y}, od0[2] = {c0.z, c0.w}, ev1[2] = {c1.x, c1.y}, od1[2] = {c1.z, c1.w};
+            const uint32_t fw0[4] = {vf0.x, vf0.y, vf0.z, vf0.w}, fw1[4] = {vf1.x, vf1.y, vf1.z, vf1.w};
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {  // blocks 4 q .. 4 q + 3
+                uint32_t a[4], b[4], c[4], d[4];
+                e2m1x8_to_f16(ev0[q], a);
+                e2m1x8_to_f16(od0[q], b);
+                e2m1x8_to_f16(ev1[q], c);
+                e2m1x8_to_f16(od1[q], d);
+                uint32_t x0[4], x1[4];
+                e4m3x4_to_f16(fw0[2 * q], x0[0], x0[1]);
+                e4m3x4_to_f16(fw0[2 * q + 1], x0[2], x0[3]);
+                e4m3x4_to_f16(fw1[2 * q], x1[0], x1[1]);
+                e4m3x4_to_f16(fw1[2 * q + 1], x1[2], x1[3]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t a0 = __byte_perm(a[k], b[k], 0x5410), a1 = __byte_perm(a[k], b[k], 0x7632);
+                    const uint32_t a2 = __byte_perm(c[k], d[k], 0x5410), a3 = __byte_perm(c[k], d[k], 0x7632);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma16816(o[n][4 * q + k], a0, a1, a2, a3, hmul2u(pb[n][0], x0[k]), hmul2u(pb[n][1], x1[k]));
+                }
+            }
+            __syncwarp();  // every lane has read the group before its stage is filled again
+            issue(cur);
+        }
+
+        // ---- the warps' results into shared memory: O[col][d] with d = 16 b + 2 g + (element / 2)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int c = 8 * n + 2 * i4 + k;
+                float t = l[n][k];
+#pragma unroll
+                for (int x = 4; x <= 16; x <<= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, x);
+                if (g == 0) {
+                    sh.m[w][c] = m[n][k];
+                    sh.l[w][c] = t;
+                }
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                    *reinterpret_cast<float2*>(&sh.o[w][c][16 * b + 2 * g]) = make_float2(o[n][b][k] * vmax, o[n][b][2 + k] * vmax);
+            }
+        }
+        __syncthreads();
+        const bool complete = cw.ja == 0 && cw.jb == cw.r.n;
+        const uint64_t u0 = pre[cw.b] + (uint64_t)cw.row * cw.r.n;  // the row's first unit
+        float* const parts = reinterpret_cast<float*>(p.ws + 64 + ATTN_MAX_CTAS);
+        auto store = [&](int c, float (&y)[4], float M, float L) {
+            const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] *= inv;
+            if (p.rotate) rotate_warp(y, lane);
+            const int j = (col0 + c) / p.group, hq_ = head * p.group + (col0 + c) - j * p.group;
+            const int64_t row = cw.r.q0 + j;
+            T* out = static_cast<T*>(p.out) + row * p.o_ts + (int64_t)hq_ * p.o_hs;
+            const T h[4] = {from_f32<DT>(y[0]), from_f32<DT>(y[1]), from_f32<DT>(y[2]), from_f32<DT>(y[3])};
+            *reinterpret_cast<uint2*>(out + 4 * lane) = *reinterpret_cast<const uint2*>(h);
+            if (p.lse && lane == 0)
+                p.lse[row * ((int64_t)p.Hkv * p.group) + hq_] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        };
+        // partial results: CTA c's slot 0 for a row that began before it, slot 1 for one that goes on after it
+        float* const mine = parts + (size_t)(2 * blockIdx.x + (cw.ja == 0 ? 1 : 0)) * ATTN_PART;
+        for (int c = w; c < tile_cols; c += W) {
+            float M = ATTN_NONE, L = 0.0f, y[4] = {};
+#pragma unroll
+            for (int k = 0; k < W; ++k) M = fmaxf(M, sh.m[k][c]);
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                const float f = ex2(sh.m[k][c] - M);
+                const float4 v = *reinterpret_cast<const float4*>(&sh.o[k][c][4 * lane]);
+                L += f * sh.l[k][c];
+                y[0] += f * v.x;
+                y[1] += f * v.y;
+                y[2] += f * v.z;
+                y[3] += f * v.w;
+            }
+            if (complete) {
+                store(c, y, M, L);
+            } else {
+                __stcg(reinterpret_cast<float4*>(mine + c * 128 + 4 * lane), make_float4(y[0], y[1], y[2], y[3]));
+                if (lane == 0) __stcg(reinterpret_cast<float2*>(mine + ATTN_MAX_NC * 128 + 2 * c), make_float2(M, L));
+            }
+        }
+        if (!complete) {
+            // the CTA that arrives last joins the row's partial results, in the order of its CTAs
+            const uint32_t first = cta_of(sc, u0), last = cta_of(sc, u0 + cw.r.n - 1);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const uint32_t seen = atomicAdd(p.ws + 64 + first, 1u);
+                sh.last = seen == last - first;
+                if (sh.last) p.ws[64 + first] = 0;  // rest state
+            }
+            __syncthreads();
+            if (sh.last) {
+                __threadfence();
+                for (int c = w; c < tile_cols; c += W) {
+                    float M = ATTN_NONE, L = 0.0f, y[4] = {};
+                    for (uint32_t k = first; k <= last; ++k) {
+                        const float* part = parts + (size_t)(2 * k + (k == first ? 1 : 0)) * ATTN_PART;
+                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part + ATTN_MAX_NC * 128 + 2 * c));
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(part + c * 128 + 4 * lane));
+                        const float t = fmaxf(M, ml.x), fa = ex2(M - t), fb = ex2(ml.x - t);
+                        M = t;
+                        L = L * fa + ml.y * fb;
+                        y[0] = y[0] * fa + v.x * fb;
+                        y[1] = y[1] * fa + v.y * fb;
+                        y[2] = y[2] * fa + v.z * fb;
+                        y[3] = y[3] * fa + v.w * fb;
+                    }
+                    store(c, y, M, L);
+                }
+            }
+        }
+        __syncthreads();  // the merge buffer and q are free again
     }
 }
 
-size_t attn_workspace_bytes() { return 256; }
+// ------------------------------------------------------------------ launch
+// Words: [0..3] as the grouped call's workspace (only [2], the error word, is
+// used), [64 ..] arrivals per CTA, then two partial results per CTA.
+size_t attn_workspace_bytes() { return 4 * (64 + (size_t)ATTN_MAX_CTAS + 2 * (size_t)ATTN_MAX_CTAS * ATTN_PART); }
+
+#ifndef HQ_ATTN_W1
+#define HQ_ATTN_W1 8
+#define HQ_ATTN_B1 2
+#define HQ_ATTN_W2 4
+#define HQ_ATTN_B2 2
+#endif
+template <int DT, int NT, int W, int MINB> static int launch_t(const AttnParams& p, int sms, cudaStream_t st) {
+    auto kernel = kv4_attention_kernel<DT, NT, W, MINB>;
+    const size_t smem = sizeof(AttnShared<NT, W>) + 8 * ((size_t)p.B + 1);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)(sizeof(AttnShared<NT, W>) + 8 * (HQ_KV_MAX_REQUESTS + 1)));
+    if (e != cudaSuccess) return (int)e;
+    int grid = sms * MINB;
+    if (grid > ATTN_MAX_CTAS) grid = ATTN_MAX_CTAS;
+    kernel<<<grid, 32 * W, smem, st>>>(p);
+    return (int)cudaPeekAtLastError();
+}
 
 int launch_attn(int dtype, const AttnParams& p, int sms, cudaStream_t st) {
-    (void)sms;
-    const dim3 grid((unsigned)p.B, (unsigned)p.Hkv, (unsigned)((p.q_len * p.group + ATTN_COLS - 1) / ATTN_COLS));
-    if (dtype == HQ_DT_BF16) kv4_attention_kernel<HQ_DT_BF16><<<grid, 32 * ATTN_WARPS, 0, st>>>(p);
-    else kv4_attention_kernel<HQ_DT_F16><<<grid, 32 * ATTN_WARPS, 0, st>>>(p);
-    return (int)cudaPeekAtLastError();
+    const bool wide = (int64_t)p.q_len * p.group > 8;
+    if (dtype == HQ_DT_BF16)
+        return wide ? launch_t<HQ_DT_BF16, 2, HQ_ATTN_W2, HQ_ATTN_B2>(p, sms, st) : launch_t<HQ_DT_BF16, 1, HQ_ATTN_W1, HQ_ATTN_B1>(p, sms, st);
+    return wide ? launch_t<HQ_DT_F16, 2, HQ_ATTN_W2, HQ_ATTN_B2>(p, sms, st) : launch_t<HQ_DT_F16, 1, HQ_ATTN_W1, HQ_ATTN_B1>(p, sms, st);
 }
 
 }  // namespace hq

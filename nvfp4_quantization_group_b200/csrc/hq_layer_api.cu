@@ -323,7 +323,7 @@ hq_status hq_kv4_attention(int dtype, const void* q, int64_t q_token_stride, int
     const int shift = page_shift_of(page_size);
     if (shift < 0 || window < 0 || sinks < 0 || !(fabsf(scale) <= 1e30f)) return HQ_ERR_UNSUPPORTED;
     if (Tq < 0 || Tq > kMaxRows || B < 0 || B > HQ_KV_MAX_REQUESTS || Hkv <= 0 || Hq <= 0 || Hq % Hkv || q_len < 1 ||
-        table_width < 0 || (table_width << shift) > kMaxRows)
+        table_width < 0 || table_width > (1 << 26) || (table_width << shift) > (1 << 30))
         return HQ_ERR_SHAPE;
     if ((int64_t)q_len * (Hq / Hkv) > 65536 || !hq_kv4_cache_bytes(num_pages, page_size, Hkv)) return HQ_ERR_SHAPE;
     if (!cu_q && Tq < (int64_t)B * q_len) return HQ_ERR_SHAPE;
