@@ -15,7 +15,11 @@
 //  * for V the weights are scaled instead: P (FP16) times the tokens' block
 //    scales of that block, half as many multiplications as V's codes.
 // The cache's byte order gives each lane its operands of a group as 16-byte
-// pieces (four for the codes, three for the block scales).
+// pieces (four for the codes, three for the block scales).  A warp takes one
+// or two groups (a unit) at a time, copied into its own ring by bulk copies that
+// run one unit ahead, so warps never wait for one another inside
+// a row; both groups of a unit that every column sees go through one stretch
+// of code.
 //
 // The running maximum moves only when a score exceeds it by 5 (in powers of
 // two), so the usual group needs no exchange between lanes: weights stay at
@@ -25,32 +29,36 @@
 
 namespace hq {
 
-#ifndef HQ_ATTN_STAGES
-#define HQ_ATTN_STAGES 3
+#ifndef HQ_ATTN_FEW
+#define HQ_ATTN_FEW 2
 #endif
-constexpr int ATTN_STAGES = HQ_ATTN_STAGES;       // groups in flight per warp
+#ifndef HQ_ATTN_STAGES
+#define HQ_ATTN_STAGES 2
+#endif
+constexpr int ATTN_STAGES = HQ_ATTN_STAGES;  // units in flight per warp
 constexpr int ATTN_MAX_CTAS = 1024;  // workspace: CTAs of a launch at most
 constexpr int ATTN_MAX_NC = 16;
 constexpr int ATTN_PART = ATTN_MAX_NC * (128 + 2);  // floats of one partial result
 constexpr float ATTN_NONE = -1e30f;  // running maximum before any token
 
 // ---------------------------------------------------------------- schedule
-// Units are groups of 16 tokens, numbered request by request, then (head,
-// column tile) row by row, then group by group.  CTA c of G takes units
+// Units of one or two groups (16 << us tokens, us = 0 or 1) are numbered request by request, then (head, column
+// tile) row by row, then in the order of the tokens.  CTA c of G takes units
 // [U c / G, U (c + 1) / G): the same load for every CTA whatever the lengths.
 struct Request {
     int q0, nq;       // first row of q, query tokens
     int len;          // tokens (clamped to the block table's row)
     int last;         // position of the last query
     int tiles;        // column tiles
-    int sink_groups;  // groups of the first tokens, before the window's
-    int first_group;  // the window's first group
-    int n;            // groups per row (at least 1 where there are queries)
+    int sink_units;   // units of the first tokens, before the window's
+    int first_unit;   // the window's first unit
+    int n;            // units per row (at least 1 where there are queries)
     bool bad;         // the length exceeds the block table's row
 };
 
-__device__ __forceinline__ Request attn_request(const AttnParams& p, int b, int nc) {
+__device__ __forceinline__ Request attn_request(const AttnParams& p, int b, int nc, int us) {
     Request r;
+    const int ut = 16 << us;
     int64_t a = p.cu_q ? p.cu_q[b] : (int64_t)b * p.q_len, e = p.cu_q ? p.cu_q[b + 1] : a + p.q_len;
     a = a < 0 ? 0 : a;
     e = e > p.Tq ? p.Tq : e;
@@ -65,17 +73,17 @@ __device__ __forceinline__ Request attn_request(const AttnParams& p, int b, int 
     // the window's first token (lengths are below 2^30: host check)
     const int64_t first = (int64_t)r.last - r.nq + 1 - p.window + 1;
     const int lo = p.window > 0 && first > 0 ? (int)min(first, (int64_t)r.len) : 0;
-    r.first_group = lo >> 4;
-    r.sink_groups = min((min(p.sinks, lo) + 15) >> 4, r.first_group);
-    r.n = r.nq ? max(1, r.sink_groups + ((r.len + 15) >> 4) - r.first_group) : 0;
+    r.first_unit = lo >> (4 + us);
+    r.sink_units = min((min(p.sinks, lo) + ut - 1) >> (4 + us), r.first_unit);
+    r.n = r.nq ? max(1, r.sink_units + ((r.len + ut - 1) >> (4 + us)) - r.first_unit) : 0;
     return r;
 }
 
-// A CTA's walk over its pieces: a piece is a run of groups of one row.
+// A CTA's walk over its pieces: a piece is a run of units of one row.
 struct Walk {
     Request r;
-    int b, row;           // request, row (head, column tile) of it
-    int ja, jb;           // groups of the piece: [ja, jb) of r.n
+    int b, row, head;     // request, row (head, column tile) of it, the row's head
+    int ja, jb;           // units of the piece: [ja, jb) of r.n
     uint64_t at, end;     // next unit, end of the CTA's units
     bool live;
 };
@@ -89,16 +97,17 @@ __device__ __forceinline__ uint64_t cta_first(const Sched& s, uint32_t c) { retu
 // The CTA that holds unit u.
 __device__ __forceinline__ uint32_t cta_of(const Sched& s, uint64_t u) { return (uint32_t)(((u + 1) * s.G - 1) / s.U); }
 
-__device__ __forceinline__ void walk_piece(const AttnParams& p, const uint64_t* pre, int nc, Walk& w) {
+__device__ __forceinline__ void walk_piece(const uint64_t* pre, Walk& w) {
     w.live = w.at < w.end;
     if (!w.live) return;
     const uint64_t in = w.at - pre[w.b];
     w.row = (int)(in / (uint32_t)w.r.n);
+    w.head = w.row / w.r.tiles;
     w.ja = (int)(in - (uint64_t)w.row * w.r.n);
     const uint64_t left = w.end - w.at;
     w.jb = left < (uint64_t)(w.r.n - w.ja) ? w.ja + (int)left : w.r.n;
 }
-__device__ __forceinline__ void walk_start(const AttnParams& p, const uint64_t* pre, int nc, uint64_t at, uint64_t end,
+__device__ __forceinline__ void walk_start(const AttnParams& p, const uint64_t* pre, int nc, int us, uint64_t at, uint64_t end,
                                            Walk& w) {
     w.at = at;
     w.end = end;
@@ -111,17 +120,17 @@ __device__ __forceinline__ void walk_start(const AttnParams& p, const uint64_t* 
         else lo = mid + 1;
     }
     w.b = lo;
-    w.r = attn_request(p, lo, nc);
-    walk_piece(p, pre, nc, w);
+    w.r = attn_request(p, lo, nc, us);
+    walk_piece(pre, w);
 }
-__device__ __forceinline__ void walk_next(const AttnParams& p, const uint64_t* pre, int nc, Walk& w) {
+__device__ __forceinline__ void walk_next(const AttnParams& p, const uint64_t* pre, int nc, int us, Walk& w) {
     w.at += (uint64_t)(w.jb - w.ja);
     if (w.at < w.end && w.at >= pre[w.b + 1]) {
         do ++w.b;
         while (w.at >= pre[w.b + 1]);
-        w.r = attn_request(p, w.b, nc);
+        w.r = attn_request(p, w.b, nc, us);
     }
-    walk_piece(p, pre, nc, w);
+    walk_piece(pre, w);
 }
 
 // ------------------------------------------------------------------ device
@@ -147,6 +156,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with a zero addend.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
@@ -195,16 +211,177 @@ __device__ __forceinline__ void rotate_warp(float (&y)[4], int lane) {
 // Shared memory of a CTA of W warps with NC columns.
 template <int NT, int W> struct AttnShared {
     static constexpr int NC = 8 * NT, OS = 132;  // columns; padded row of the merge buffer (free of bank conflicts)
-    alignas(128) uint8_t ring[W][ATTN_STAGES][KV_GROUP_BYTES];
-    float o[W][NC][OS];
-    uint32_t q[2][NC][64];  // hi and lo parts, FP16 pairs
+    alignas(128) uint8_t ring[W][ATTN_STAGES][2 * KV_GROUP_BYTES];
+    union {
+        float o[W / 2][NC][OS];           // results of the lower half's warps
+        float4 frag[W / 2][NT * 8][32];   // accumulators of the upper half's warps
+    };
+    uint4 q[NT][8][32];  // per block and lane: hi and lo parts of its four elements of column lane / 4
     float m[W][NC], l[W][NC];
     float qs[NC];  // factor of a column's scores, in powers of two
+    int pos[NC];   // a column's position
+    Walk cw;       // the CTA's current piece
+    Walk lw[W];    // the piece of each warp's next load
     uint64_t full[W][ATTN_STAGES];
     unsigned long long warp_sums[W];
     int last;
     // then the units before each request, uint64_t [B + 1]
 };
+
+// What a lane carries through a row.
+template <int NT> struct AttnState {
+    float o[NT][8][4];  // O^T: block b, rows d = 16 b + 2 g (0, 1) and + 1 (2, 3), columns 2 i, 2 i + 1
+    float m[NT][2], l[NT][2];
+    float vmax, vinv;  // largest decode scale of V so far (the accumulators are relative to it), and its inverse
+    float qs[NT][2];
+};
+
+// Scores (in powers of two) of the group at `grp`: rows g, g + 8, columns 2 i, 2 i + 1.
+template <int NT>
+__device__ __forceinline__ void attn_scores(const uint8_t* grp, const uint4 (*q)[8][32], const AttnState<NT>& a, int lane,
+                                            float (&s)[NT][4]) {
+    const int g = lane >> 2;
+    const uint4 k0 = *reinterpret_cast<const uint4*>(grp + KV_K_CODES + lane * 16);
+    const uint4 k1 = *reinterpret_cast<const uint4*>(grp + KV_K_CODES + lane * 16 + 512);
+    const uint2 f0 = *reinterpret_cast<const uint2*>(grp + KV_K_SF + g * 8);
+    const uint2 f1 = *reinterpret_cast<const uint2*>(grp + KV_K_SF + g * 8 + 64);
+    const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
+    uint32_t sf0[4], sf1[4];
+    e4m3x4_to_f16(f0.x, sf0[0], sf0[1]);
+    e4m3x4_to_f16(f0.y, sf0[2], sf0[3]);
+    e4m3x4_to_f16(f1.x, sf1[0], sf1[1]);
+    e4m3x4_to_f16(f1.y, sf1[2], sf1[3]);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
+#pragma unroll
+    for (int b2 = 0; b2 < 4; ++b2) {  // blocks 2 b2, 2 b2 + 1
+        uint32_t a0[4], a1[4];
+        e2m1x8_to_f16(kw0[b2], a0);
+        e2m1x8_to_f16(kw1[b2], a1);
+        const float2 x0 = h2f(sf0[b2]), x1 = h2f(sf1[b2]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint4 f = q[n][2 * b2 + k][lane];
+                float c[4];
+                mma16816_first(c, a0[2 * k], a1[2 * k], a0[2 * k + 1], a1[2 * k + 1], f.x, f.y);
+                mma16816(c, a0[2 * k], a1[2 * k], a0[2 * k + 1], a1[2 * k + 1], f.z, f.w);
+                const float y0 = k ? x0.y : x0.x, y1 = k ? x1.y : x1.x;
+                s[n][0] = __fmaf_rn(y0, c[0], s[n][0]);
+                s[n][1] = __fmaf_rn(y0, c[1], s[n][1]);
+                s[n][2] = __fmaf_rn(y1, c[2], s[n][2]);
+                s[n][3] = __fmaf_rn(y1, c[3], s[n][3]);
+            }
+        }
+    }
+    const float d0 = *reinterpret_cast<const float*>(grp + KV_K_DEC + 4 * g);
+    const float d1 = *reinterpret_cast<const float*>(grp + KV_K_DEC + 4 * g + 32);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        s[n][0] = __fmul_rn(s[n][0], __fmul_rn(d0, a.qs[n][0]));
+        s[n][1] = __fmul_rn(s[n][1], __fmul_rn(d0, a.qs[n][1]));
+        s[n][2] = __fmul_rn(s[n][2], __fmul_rn(d1, a.qs[n][0]));
+        s[n][3] = __fmul_rn(s[n][3], __fmul_rn(d1, a.qs[n][1]));
+    }
+}
+
+// Moves the references to scores s (N groups' worth) and value scales v.
+template <int NT, int N>
+__device__ __forceinline__ void attn_grow(AttnState<NT>& a, const float (&s)[N][NT][4], const float (&v)[N][2]) {
+    float x = a.vmax;
+#pragma unroll
+    for (int h = 0; h < N; ++h) x = max3(x, v[h][0], v[h][1]);
+    bool grow = x > a.vmax;
+    float top[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            top[n][k] = fmaxf(s[0][n][k], s[0][n][2 + k]);
+#pragma unroll
+            for (int h = 1; h < N; ++h) top[n][k] = max3(top[n][k], s[h][n][k], s[h][n][2 + k]);
+            grow |= top[n][k] - a.m[n][k] > 5.0f;
+        }
+    if (!__any_sync(0xFFFFFFFFu, grow)) return;
+#pragma unroll
+    for (int k = 4; k <= 16; k <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, k));
+    const float beta = x > 0.0f ? __fdividef(a.vmax, x) : 0.0f;
+    a.vmax = x;
+    a.vinv = x > 0.0f ? __frcp_rn(x) : 0.0f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        float f[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float t = fmaxf(a.m[n][k], top[n][k]);
+#pragma unroll
+            for (int y = 4; y <= 16; y <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, y));
+            f[k] = ex2(a.m[n][k] - t);
+            a.m[n][k] = t;
+            a.l[n][k] *= f[k];
+            f[k] *= beta;
+        }
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+            a.o[n][b][0] *= f[0];
+            a.o[n][b][1] *= f[1];
+            a.o[n][b][2] *= f[0];
+            a.o[n][b][3] *= f[1];
+        }
+    }
+}
+
+// Adds the group's weighted values.  v: decode scales of rows g, g + 8; keep0,
+// keep1: the bytes to keep of the block scales of the lane's tokens 2 i, 2 i + 1
+// and 2 i + 8, + 9.
+template <int NT, bool MASK>
+__device__ __forceinline__ void attn_values(const uint8_t* grp, AttnState<NT>& a, const float (&s)[NT][4],
+                                            const float (&v)[2], uint32_t keep0, uint32_t keep1, int lane) {
+    const float r0 = v[0] * a.vinv, r1 = v[1] * a.vinv;
+    uint4 vf0 = *reinterpret_cast<const uint4*>(grp + KV_V_SF + (lane & 3) * 16);
+    uint4 vf1 = *reinterpret_cast<const uint4*>(grp + KV_V_SF + (lane & 3) * 16 + 64);
+    if constexpr (MASK) {
+        vf0 = make_uint4(vf0.x & keep0, vf0.y & keep0, vf0.z & keep0, vf0.w & keep0);
+        vf1 = make_uint4(vf1.x & keep1, vf1.y & keep1, vf1.z & keep1, vf1.w & keep1);
+    }
+    uint32_t pb[NT][2];  // weights as the n side: column g, tokens 2 i, 2 i + 1 and 2 i + 8, + 9
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const float e0 = ex2(s[n][0] - a.m[n][0]), e1 = ex2(s[n][1] - a.m[n][1]);
+        const float e2 = ex2(s[n][2] - a.m[n][0]), e3 = ex2(s[n][3] - a.m[n][1]);
+        a.l[n][0] += e0 + e2;
+        a.l[n][1] += e1 + e3;
+        pb[n][0] = transpose8x8(pack_h2(e0 * r0, e1 * r0));
+        pb[n][1] = transpose8x8(pack_h2(e2 * r1, e3 * r1));
+    }
+    const uint4 c0 = *reinterpret_cast<const uint4*>(grp + KV_V_CODES + lane * 16);
+    const uint4 c1 = *reinterpret_cast<const uint4*>(grp + KV_V_CODES + lane * 16 + 512);
+    const uint32_t ev0[2] = {c0.x, c0.y}, od0[2] = {c0.z, c0.w}, ev1[2] = {c1.x, c1.y}, od1[2] = {c1.z, c1.w};
+    const uint32_t fw0[4] = {vf0.x, vf0.y, vf0.z, vf0.w}, fw1[4] = {vf1.x, vf1.y, vf1.z, vf1.w};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {  // blocks 4 q .. 4 q + 3
+        uint32_t ea[4], oa[4], eb[4], ob[4], x0[4], x1[4];
+        e2m1x8_to_f16(ev0[q], ea);
+        e2m1x8_to_f16(od0[q], oa);
+        e2m1x8_to_f16(ev1[q], eb);
+        e2m1x8_to_f16(od1[q], ob);
+        e4m3x4_to_f16(fw0[2 * q], x0[0], x0[1]);
+        e4m3x4_to_f16(fw0[2 * q + 1], x0[2], x0[3]);
+        e4m3x4_to_f16(fw1[2 * q], x1[0], x1[1]);
+        e4m3x4_to_f16(fw1[2 * q + 1], x1[2], x1[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t a0 = __byte_perm(ea[k], oa[k], 0x5410), a1 = __byte_perm(ea[k], oa[k], 0x7632);
+            const uint32_t a2 = __byte_perm(eb[k], ob[k], 0x5410), a3 = __byte_perm(eb[k], ob[k], 0x7632);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                mma16816(a.o[n][4 * q + k], a0, a1, a2, a3, hmul2u(pb[n][0], x0[k]), hmul2u(pb[n][1], x1[k]));
+        }
+    }
+}
 
 template <int DT, int NT, int W, int MINB>
 __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams p) {
@@ -217,101 +394,130 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, i4 = lane & 3;
 
     if (lane < S) mbar_init(&sh.full[w][lane], 1);
-    // ---- units before each request
-    unsigned long long carry = 0;
+    // ---- units before each request: units of one group while there are few
+    // (latency counts), of two otherwise (fewer turns of the loops)
+    Sched sc;
     bool bad = false;
-    for (int b0 = 0; b0 < p.B; b0 += 32 * W) {
-        const int b = b0 + tid;
-        unsigned long long v = 0;
-        if (b < p.B) {
-            const Request r = attn_request(p, b, NC);
-            v = (unsigned long long)r.tiles * p.Hkv * r.n;
-            bad |= r.bad && r.nq;
-        }
-        unsigned long long s = v;
+    int us = 0;
+    for (;; ++us) {
+        unsigned long long carry = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32 * W) {
+            const int b = b0 + tid;
+            unsigned long long v = 0;
+            if (b < p.B) {
+                const Request r = attn_request(p, b, NC, us);
+                v = (unsigned long long)r.tiles * p.Hkv * r.n;
+                bad |= r.bad && r.nq;
+            }
+            unsigned long long s = v;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long u = __shfl_up_sync(0xFFFFFFFFu, s, o);
-            if (lane >= o) s += u;
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+                if (lane >= o) s += u;
+            }
+            if (lane == 31) sh.warp_sums[w] = s;
+            __syncthreads();
+            unsigned long long before = carry, total = 0;
+            for (int k = 0; k < W; ++k) {
+                if (k < w) before += sh.warp_sums[k];
+                total += sh.warp_sums[k];
+            }
+            if (b < p.B) pre[b] = before + s - v;
+            carry += total;
+            __syncthreads();
         }
-        if (lane == 31) sh.warp_sums[w] = s;
-        __syncthreads();
-        unsigned long long before = carry, total = 0;
-        for (int k = 0; k < W; ++k) {
-            if (k < w) before += sh.warp_sums[k];
-            total += sh.warp_sums[k];
-        }
-        if (b < p.B) pre[b] = before + s - v;
-        carry += total;
-        __syncthreads();
+        if (tid == 0) pre[p.B] = carry;
+        sc.U = carry;
+        if (us == 1 || carry <= (uint64_t)HQ_ATTN_FEW * W * gridDim.x) break;
     }
-    if (tid == 0) pre[p.B] = carry;
     fence_mbar_init();
     __syncthreads();
-    Sched sc;
-    sc.U = carry;
     if (sc.U == 0) return;
-    {  // at least one group per warp of a CTA
+    {  // at least one unit per warp of a CTA
         const uint64_t most = (sc.U + W - 1) / W;
         sc.G = most < gridDim.x ? (uint32_t)most : gridDim.x;
     }
     if (blockIdx.x >= sc.G) return;
     if (bad) p.ws[2] = HQ_ERR_PAGE;  // (every CTA that is not idle reports the same)
 
-    // ---- the warp's loads run ahead of its arithmetic, across pieces
-    Walk lw, cw;
-    walk_start(p, pre, NC, cta_first(sc, blockIdx.x), cta_first(sc, blockIdx.x + 1), cw);
-    lw = cw;
-    int lj = lw.ja + w;       // next group to load of lw's piece
-    int page = -1;            // its page (prefetched), or -1
-    uint32_t stage_ok = 0;    // bit s: stage s holds a group
+    // ---- the warp's loads run ahead of its arithmetic, across pieces.  (The
+    // pieces' records live in shared memory: they are read once per unit, and in
+    // registers they would push the accumulators out.)
+    Walk& cw = sh.cw;
+    Walk& lw = sh.lw[w];
+    {
+        Walk t;
+        walk_start(p, pre, NC, us, cta_first(sc, blockIdx.x), cta_first(sc, blockIdx.x + 1), t);
+        if (tid == 0) cw = t;
+        if (lane == 0) lw = t;
+    }
+    __syncthreads();
     const int groups_shift = p.page_shift - 4;
-    const uint32_t ring0 = smem_u32(sh.ring[w][0]);
-    auto group_of = [&](const Walk& k, int j) { return j < k.r.sink_groups ? j : k.r.first_group + (j - k.r.sink_groups); };
-    auto settle = [&]() {  // move to the next piece with a group for this warp
-        while (lw.live && lj >= lw.jb) {
-            walk_next(p, pre, NC, lw);
-            lj = lw.ja + w;
-        }
+    const bool small_pages = groups_shift == 0;  // a unit's two groups lie on two pages
+    int lj = lw.ja + w;       // next unit to load of lw's piece
+    int pg[2] = {-1, -1};     // the pages of its groups (looked up one unit ahead), or -1
+    uint32_t stage_ok = 0;    // bits 2 s, 2 s + 1: stage s holds its groups
+    auto unit_of = [](const Walk& k, int j) {
+        return j < k.r.sink_units ? j : k.r.first_unit + (j - k.r.sink_units);
     };
-    auto fetch_page = [&]() {
-        page = -1;
-        if (lw.live) {
-            const int grp = group_of(lw, lj);
-            if (grp * 16 < lw.r.len) {
-                page = p.table[(int64_t)lw.b * p.width + (grp >> groups_shift)];
-                if (page < 0 || page >= p.num_pages) {
-                    page = -1;
-                    p.ws[2] = HQ_ERR_PAGE;
-                }
-            }
+    auto settle = [&]() {  // on to the next piece with a unit for this warp
+        if (!lw.live || lj < lw.jb) return;
+        Walk t = lw;
+        while (t.live && lj >= t.jb) {
+            walk_next(p, pre, NC, us, t);
+            lj = t.ja + w;
         }
+        __syncwarp();
+        if (lane == 0) lw = t;
+        __syncwarp();
     };
-    auto issue = [&](int st) {  // load the group at (lw, lj) into stage st, then look up the next one's page
-        stage_ok &= ~(1u << st);
+    auto look_up = [&]() {
+        pg[0] = pg[1] = -1;
         if (!lw.live) return;
-        if (page >= 0) {
-            const int grp = group_of(lw, lj), head = lw.row / lw.r.tiles;
-            const uint8_t* src = p.cache + ((((int64_t)page * p.Hkv + head) << groups_shift) +
-                                            (grp & ((1 << groups_shift) - 1))) * KV_GROUP_BYTES;
-            if (lane == 0) {
-                mbar_arrive_expect(&sh.full[w][st], KV_GROUP_BYTES);
-                bulk_load(ring0 + st * KV_GROUP_BYTES, src, KV_GROUP_BYTES, &sh.full[w][st]);
-            }
-            stage_ok |= 1u << st;
+        const int t = unit_of(lw, lj) << (4 + us), len = lw.r.len;
+        const int32_t* const row = p.table + (int64_t)lw.b * p.width;
+        if (t < len) pg[0] = row[t >> p.page_shift];
+        if (us && t + 16 < len) pg[1] = small_pages ? row[(t >> 4) + 1] : pg[0];
+    };
+    // load the unit at (lw, lj) into stage st, then look up the next one's pages
+    auto issue = [&](int st) {
+        stage_ok &= ~(3u << (2 * st));
+        if (!lw.live) return;
+        const uint32_t ok = ((uint32_t)pg[0] < (uint64_t)p.num_pages ? 1u : 0u) |
+                            ((uint32_t)pg[1] < (uint64_t)p.num_pages ? 2u : 0u);  // (-1 is no page either)
+        const int at = unit_of(lw, lj) << us;
+        if (ok != 3) {  // behind the request's end, or a bad entry
+            const int len = lw.r.len;
+            if ((!(ok & 1) && 16 * at < len) || (us && !(ok & 2) && 16 * at + 16 < len)) p.ws[2] = HQ_ERR_PAGE;
         }
+        if (ok && lane == 0) {
+            const uint32_t page_groups = (uint32_t)p.Hkv << groups_shift, head = (uint32_t)lw.head << groups_shift;
+            const uint32_t dst = smem_u32(sh.ring[w][st]);
+            const uint8_t* const a = p.cache + ((uint64_t)(uint32_t)pg[0] * page_groups + head +
+                                                ((uint32_t)at & ((1u << groups_shift) - 1))) * KV_GROUP_BYTES;
+            mbar_arrive_expect(&sh.full[w][st], ok == 3 ? 2 * KV_GROUP_BYTES : KV_GROUP_BYTES);
+            if (ok == 3 && !small_pages) {
+                bulk_load(dst, a, 2 * KV_GROUP_BYTES, &sh.full[w][st]);
+            } else {
+                if (ok & 1) bulk_load(dst, a, KV_GROUP_BYTES, &sh.full[w][st]);
+                if (ok & 2)  // (pages of one group: the head's group on the second page)
+                    bulk_load(dst + KV_GROUP_BYTES, p.cache + ((uint64_t)(uint32_t)pg[1] * page_groups + head) * KV_GROUP_BYTES,
+                              KV_GROUP_BYTES, &sh.full[w][st]);
+            }
+        }
+        stage_ok |= ok << (2 * st);
         lj += W;
         settle();
-        fetch_page();
+        look_up();
     };
     settle();
-    fetch_page();
+    look_up();
     for (int s = 0; s < S; ++s) issue(s);
     int st = 0;
     uint32_t phases = 0;  // bit s: parity of stage s's next completion
 
-    for (; cw.live; walk_next(p, pre, NC, cw)) {
-        const int head = cw.row / cw.r.tiles, col0 = (cw.row - head * cw.r.tiles) * NC, cols = cw.r.nq * p.group;
+    while (cw.live) {
+        const int head = cw.head, col0 = (cw.row - head * cw.r.tiles) * NC, cols = cw.r.nq * p.group;
         const int tile_cols = min(NC, cols - col0);
         // ---- q: rotate, split into two FP16 parts, relative to the column's largest power of two
         for (int c = w; c < NC; c += W) {
@@ -319,8 +525,10 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
             if (c < tile_cols) {
                 const int j = (col0 + c) / p.group, hh = (col0 + c) - j * p.group;
                 const T* x = static_cast<const T*>(p.q) + (int64_t)(cw.r.q0 + j) * p.q_ts + (int64_t)(head * p.group + hh) * p.q_hs;
+                const uint2 u = *reinterpret_cast<const uint2*>(x + 4 * lane);
+                const T* h = reinterpret_cast<const T*>(&u);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = to_f32(x[4 * lane + e]);
+                for (int e = 0; e < 4; ++e) y[e] = to_f32(h[e]);
             }
             if (p.rotate) rotate_warp(y, lane);
             float a = max3(fmaxf(fabsf(y[0]), fabsf(y[1])), fabsf(y[2]), fabsf(y[3]));
@@ -337,232 +545,154 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                 hi[e] = __half2float(__float2half_rn(v));
                 lo[e] = __fsub_rn(v, hi[e]);
             }
-            *reinterpret_cast<uint2*>(&sh.q[0][c][2 * lane]) = make_uint2(pack_h2(hi[0], hi[1]), pack_h2(hi[2], hi[3]));
-            *reinterpret_cast<uint2*>(&sh.q[1][c][2 * lane]) = make_uint2(pack_h2(lo[0], lo[1]), pack_h2(lo[2], lo[3]));
-            if (lane == 0) sh.qs[c] = up * p.scale * 1.4426950408889634f;
+            // elements 4 lane .. + 3: block lane / 4, quad lane % 4 of column c
+            sh.q[c >> 3][lane >> 2][(c & 7) * 4 + (lane & 3)] =
+                make_uint4(pack_h2(hi[0], hi[1]), pack_h2(hi[2], hi[3]), pack_h2(lo[0], lo[1]), pack_h2(lo[2], lo[3]));
+            if (lane == 0) {
+                sh.qs[c] = up * p.scale * 1.4426950408889634f;
+                sh.pos[c] = cw.r.last - (cw.r.nq - 1 - min(col0 + c, cols - 1) / p.group);
+            }
         }
         __syncthreads();
-        uint2 qf[2][NT][8];  // n side of the first product: column g, elements 16 b + 4 i .. + 3
-        float qs[NT][2];
-        int pos[NT][2], pos_min = 0x7FFFFFFF, pos_max = -1;
+        AttnState<NT> a;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                qf[0][n][b] = *reinterpret_cast<const uint2*>(&sh.q[0][8 * n + g][8 * b + 2 * i4]);
-                qf[1][n][b] = *reinterpret_cast<const uint2*>(&sh.q[1][8 * n + g][8 * b + 2 * i4]);
-            }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int c = 8 * n + 2 * i4 + k;
-                qs[n][k] = sh.qs[c];
-                pos[n][k] = cw.r.last - (cw.r.nq - 1 - min(col0 + c, cols - 1) / p.group);
+                a.qs[n][k] = sh.qs[c];
+                a.m[n][k] = ATTN_NONE;
+                a.l[n][k] = 0.0f;
             }
-        }
-        pos_min = cw.r.last - (cw.r.nq - 1 - col0 / p.group);
-        pos_max = cw.r.last - (cw.r.nq - 1 - (col0 + tile_cols - 1) / p.group);
-
-        float o[NT][8][4], m[NT][2], l[NT][2], vmax = 0.0f, vinv = 0.0f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int b = 0; b < 8; ++b)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[n][b][e] = 0.0f;
-            m[n][0] = m[n][1] = ATTN_NONE;
-            l[n][0] = l[n][1] = 0.0f;
+                for (int e = 0; e < 4; ++e) a.o[n][b][e] = 0.0f;
         }
+        const int pos_min = sh.pos[0], pos_max = sh.pos[NC - 1];
+        a.vmax = a.vinv = 0.0f;
 
         for (int j = cw.ja + w; j < cw.jb; j += W) {
             const int cur = st;
             st = st + 1 == S ? 0 : st + 1;
-            if (!(stage_ok >> cur & 1u)) {  // no page: the tokens count as not seen
+            const uint32_t ok = stage_ok >> (2 * cur) & 3u;
+            if (!ok) {  // no page: the tokens count as not seen
                 issue(cur);
                 continue;
             }
-            // bounded by the copy's own end; a copy that never ends leaves the loop with an error (about 2 s)
-            bool got = mbar_try_wait_sleep(&sh.full[w][cur], phases >> cur & 1u, 1000000u);
-            for (int spin = 0; !got && spin < 2000; ++spin)
-                got = mbar_try_wait_sleep(&sh.full[w][cur], phases >> cur & 1u, 1000000u);
-            if (!got) p.ws[2] = HQ_ERR_TIMEOUT;
+            // a copy ends by itself; the limit (about 2 s) only keeps the wait from being endless
+            if (!mbar_wait_bounded(&sh.full[w][cur], phases >> cur & 1u, 2000000u)) p.ws[2] = HQ_ERR_TIMEOUT;
             phases ^= 1u << cur;
-            const uint8_t* const grp = sh.ring[w][cur];
-            const int t0 = group_of(cw, j) * 16;
-
-            // ---- scores
-            float s[NT][4];
+            const uint8_t* const unit = sh.ring[w][cur];
+            const int t0 = unit_of(cw, j) << (4 + us);
+            if (ok == 3u && t0 + 31 <= pos_min && (p.window == 0 || pos_max - t0 < p.window || t0 + 31 < p.sinks)) {
+                // every column sees every token
+                float s[2][NT][4], v[2][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
-            {
-                const uint4 k0 = *reinterpret_cast<const uint4*>(grp + KV_K_CODES + g * 64 + i4 * 16);
-                const uint4 k1 = *reinterpret_cast<const uint4*>(grp + KV_K_CODES + g * 64 + i4 * 16 + 512);
-                const uint2 f0 = *reinterpret_cast<const uint2*>(grp + KV_K_SF + g * 8);
-                const uint2 f1 = *reinterpret_cast<const uint2*>(grp + KV_K_SF + g * 8 + 64);
-                const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
-                uint32_t sf0[4], sf1[4];
-                e4m3x4_to_f16(f0.x, sf0[0], sf0[1]);
-                e4m3x4_to_f16(f0.y, sf0[2], sf0[3]);
-                e4m3x4_to_f16(f1.x, sf1[0], sf1[1]);
-                e4m3x4_to_f16(f1.y, sf1[2], sf1[3]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {  // blocks 2 q, 2 q + 1
-                    uint32_t a0[4], a1[4];
-                    e2m1x8_to_f16(kw0[q], a0);
-                    e2m1x8_to_f16(kw1[q], a1);
-                    const float2 x0 = h2f(sf0[q]), x1 = h2f(sf1[q]);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint2 hi = qf[0][n][2 * q + k], lo = qf[1][n][2 * q + k];
-                            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma16816(c, a0[2 * k], a1[2 * k], a0[2 * k + 1], a1[2 * k + 1], hi.x, hi.y);
-                            mma16816(c, a0[2 * k], a1[2 * k], a0[2 * k + 1], a1[2 * k + 1], lo.x, lo.y);
-                            const float y0 = k ? x0.y : x0.x, y1 = k ? x1.y : x1.x;
-                            s[n][0] = __fmaf_rn(y0, c[0], s[n][0]);
-                            s[n][1] = __fmaf_rn(y0, c[1], s[n][1]);
-                            s[n][2] = __fmaf_rn(y1, c[2], s[n][2]);
-                            s[n][3] = __fmaf_rn(y1, c[3], s[n][3]);
-                        }
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    const uint8_t* grp = unit + h * KV_GROUP_BYTES;
+                    attn_scores<NT>(grp, sh.q, a, lane, s[h]);
+                    v[h][0] = *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g);
+                    v[h][1] = *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g + 32);
                 }
-                const float d0 = *reinterpret_cast<const float*>(grp + KV_K_DEC + 4 * g);
-                const float d1 = *reinterpret_cast<const float*>(grp + KV_K_DEC + 4 * g + 32);
+                attn_grow<NT, 2>(a, s, v);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    s[n][0] = __fmul_rn(s[n][0], __fmul_rn(d0, qs[n][0]));
-                    s[n][1] = __fmul_rn(s[n][1], __fmul_rn(d0, qs[n][1]));
-                    s[n][2] = __fmul_rn(s[n][2], __fmul_rn(d1, qs[n][0]));
-                    s[n][3] = __fmul_rn(s[n][3], __fmul_rn(d1, qs[n][1]));
-                }
-            }
-            float v0 = *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g);
-            float v1 = *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g + 32);
-            uint4 vf0 = *reinterpret_cast<const uint4*>(grp + KV_V_SF + i4 * 16);
-            uint4 vf1 = *reinterpret_cast<const uint4*>(grp + KV_V_SF + i4 * 16 + 64);
-            const bool whole = t0 + 15 <= pos_min && (p.window == 0 || pos_max - t0 < p.window || t0 + 15 < p.sinks);
-            if (!whole) {
-                const int ta = t0 + g, tb = ta + 8;
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int q = pos[n][k];
-                        if (!(ta <= q && (p.window == 0 || q - ta < p.window || ta < p.sinks))) s[n][k] = -INFINITY;
-                        if (!(tb <= q && (p.window == 0 || q - tb < p.window || tb < p.sinks))) s[n][2 + k] = -INFINITY;
-                    }
-                // tokens behind the last query's position may hold anything: their value scales count as zero
-                if (ta > pos_max) v0 = 0.0f;
-                if (tb > pos_max) v1 = 0.0f;
-                const int e = pos_max - t0 - 2 * i4;  // the lane's even token is real if e >= 0, the odd one if e >= 1
-                const uint32_t keep0 = (e >= 0 ? 0x00FF00FFu : 0u) | (e >= 1 ? 0xFF00FF00u : 0u);
-                const uint32_t keep1 = (e >= 8 ? 0x00FF00FFu : 0u) | (e >= 9 ? 0xFF00FF00u : 0u);
-                vf0 = make_uint4(vf0.x & keep0, vf0.y & keep0, vf0.z & keep0, vf0.w & keep0);
-                vf1 = make_uint4(vf1.x & keep1, vf1.y & keep1, vf1.z & keep1, vf1.w & keep1);
-            }
-            // ---- move the references when a score or a value scale has outgrown them
-            bool grow = v0 * vinv > 1.0001f || v1 * vinv > 1.0001f || vmax == 0.0f;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                grow |= fmaxf(s[n][0], s[n][2]) > m[n][0] + 5.0f || fmaxf(s[n][1], s[n][3]) > m[n][1] + 5.0f;
-            if (__any_sync(0xFFFFFFFFu, grow)) {
-                float v = fmaxf(v0, v1);
-#pragma unroll
-                for (int x = 4; x <= 16; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, x));
-                v = fmaxf(v, vmax);
-                const float beta = v > 0.0f ? vmax / v : 0.0f;
-                vmax = v;
-                vinv = v > 0.0f ? 1.0f / v : 0.0f;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float f[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float t = fmaxf(s[n][k], s[n][2 + k]);
-#pragma unroll
-                        for (int x = 4; x <= 16; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, x));
-                        t = fmaxf(t, m[n][k]);
-                        f[k] = ex2(m[n][k] - t);
-                        m[n][k] = t;
-                        l[n][k] *= f[k];
-                        f[k] *= beta;
-                    }
-#pragma unroll
-                    for (int b = 0; b < 8; ++b) {
-                        o[n][b][0] *= f[0];
-                        o[n][b][1] *= f[1];
-                        o[n][b][2] *= f[0];
-                        o[n][b][3] *= f[1];
-                    }
-                }
-            }
-            // ---- weights, as the n side of the second product
-            const float r0 = v0 * vinv, r1 = v1 * vinv;
-            uint32_t pb[NT][2];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float e0 = ex2(s[n][0] - m[n][0]), e1 = ex2(s[n][1] - m[n][1]);
-                const float e2 = ex2(s[n][2] - m[n][0]), e3 = ex2(s[n][3] - m[n][1]);
-                l[n][0] += e0 + e2;
-                l[n][1] += e1 + e3;
-                pb[n][0] = transpose8x8(pack_h2(e0 * r0, e1 * r0));
-                pb[n][1] = transpose8x8(pack_h2(e2 * r1, e3 * r1));
-            }
-            // ---- values
-            const uint4 c0 = *reinterpret_cast<const uint4*>(grp + KV_V_CODES + lane * 16);
-            const uint4 c1 = *reinterpret_cast<const uint4*>(grp + KV_V_CODES + lane * 16 + 512);
-            const uint32_t ev0[2] = {c0.x, c0.y}, od0[2] = {c0.z, c0.w}, ev1[2] = {c1.x, c1.y}, od1[2] = {c1.z, c1.w};
-            const uint32_t fw0[4] = {vf0.x, vf0.y, vf0.z, vf0.w}, fw1[4] = {vf1.x, vf1.y, vf1.z, vf1.w};
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {  // blocks 4 q .. 4 q + 3
-                uint32_t a[4], b[4], c[4], d[4];
-                e2m1x8_to_f16(ev0[q], a);
-                e2m1x8_to_f16(od0[q], b);
-                e2m1x8_to_f16(ev1[q], c);
-                e2m1x8_to_f16(od1[q], d);
-                uint32_t x0[4], x1[4];
-                e4m3x4_to_f16(fw0[2 * q], x0[0], x0[1]);
-                e4m3x4_to_f16(fw0[2 * q + 1], x0[2], x0[3]);
-                e4m3x4_to_f16(fw1[2 * q], x1[0], x1[1]);
-                e4m3x4_to_f16(fw1[2 * q + 1], x1[2], x1[3]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t a0 = __byte_perm(a[k], b[k], 0x5410), a1 = __byte_perm(a[k], b[k], 0x7632);
-                    const uint32_t a2 = __byte_perm(c[k], d[k], 0x5410), a3 = __byte_perm(c[k], d[k], 0x7632);
+                for (int h = 0; h < 2; ++h) attn_values<NT, false>(unit + h * KV_GROUP_BYTES, a, s[h], v[h], 0u, 0u, lane);
+            } else {
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    if (!(ok >> h & 1u)) continue;
+                    const uint8_t* grp = unit + h * KV_GROUP_BYTES;
+                    float s[1][NT][4], v[1][2];
+                    attn_scores<NT>(grp, sh.q, a, lane, s[0]);
+                    const int t1 = t0 + 16 * h, ta = t1 + g, tb = ta + 8;
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        mma16816(o[n][4 * q + k], a0, a1, a2, a3, hmul2u(pb[n][0], x0[k]), hmul2u(pb[n][1], x1[k]));
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int q = sh.pos[8 * n + 2 * i4 + k];
+                            if (!(ta <= q && (p.window == 0 || q - ta < p.window || ta < p.sinks))) s[0][n][k] = -INFINITY;
+                            if (!(tb <= q && (p.window == 0 || q - tb < p.window || tb < p.sinks))) s[0][n][2 + k] = -INFINITY;
+                        }
+                    // tokens behind the last query's position may hold anything: their value scales count as zero
+                    v[0][0] = ta > pos_max ? 0.0f : *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g);
+                    v[0][1] = tb > pos_max ? 0.0f : *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g + 32);
+                    const int e = pos_max - t1 - 2 * i4;  // the lane's even token is real if e >= 0, the odd one if e >= 1
+                    const uint32_t keep0 = (e >= 0 ? 0x00FF00FFu : 0u) | (e >= 1 ? 0xFF00FF00u : 0u);
+                    const uint32_t keep1 = (e >= 8 ? 0x00FF00FFu : 0u) | (e >= 9 ? 0xFF00FF00u : 0u);
+                    attn_grow<NT, 1>(a, s, v);
+                    attn_values<NT, true>(grp, a, s[0], v[0], keep0, keep1, lane);
                 }
             }
-            __syncwarp();  // every lane has read the group before its stage is filled again
+            __syncwarp();  // every lane has read the unit before its stage is filled again
             issue(cur);
         }
 
-        // ---- the warps' results into shared memory: O[col][d] with d = 16 b + 2 g + (element / 2)
+        // ---- join the warps: common references, then the upper half's accumulators into the lower half's
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float t = a.l[n][k];
+#pragma unroll
+                for (int x = 4; x <= 16; x <<= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, x);
+                if (g == 0) {
+                    sh.m[w][8 * n + 2 * i4 + k] = a.m[n][k];
+                    sh.l[w][8 * n + 2 * i4 + k] = t;
+                }
+            }
+        __syncthreads();
+        float M[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int c = 8 * n + 2 * i4 + k;
-                float t = l[n][k];
+                M[n][k] = ATTN_NONE;
 #pragma unroll
-                for (int x = 4; x <= 16; x <<= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, x);
-                if (g == 0) {
-                    sh.m[w][c] = m[n][k];
-                    sh.l[w][c] = t;
+                for (int x = 0; x < W; ++x) M[n][k] = fmaxf(M[n][k], sh.m[x][c]);
+                const float f = ex2(a.m[n][k] - M[n][k]) * a.vmax;
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {
+                    a.o[n][b][k] *= f;
+                    a.o[n][b][2 + k] *= f;
                 }
+            }
+            if (w >= W / 2) {
 #pragma unroll
                 for (int b = 0; b < 8; ++b)
-                    *reinterpret_cast<float2*>(&sh.o[w][c][16 * b + 2 * g]) = make_float2(o[n][b][k] * vmax, o[n][b][2 + k] * vmax);
+                    sh.frag[w - W / 2][8 * n + b][lane] = make_float4(a.o[n][b][0], a.o[n][b][1], a.o[n][b][2], a.o[n][b][3]);
             }
+        }
+        __syncthreads();
+        if (w < W / 2) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {
+                    const float4 v = sh.frag[w][8 * n + b][lane];
+                    a.o[n][b][0] += v.x;
+                    a.o[n][b][1] += v.y;
+                    a.o[n][b][2] += v.z;
+                    a.o[n][b][3] += v.w;
+                }
+        }
+        __syncthreads();
+        if (w < W / 2) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        *reinterpret_cast<float2*>(&sh.o[w][8 * n + 2 * i4 + k][16 * b + 2 * g]) =
+                            make_float2(a.o[n][b][k], a.o[n][b][2 + k]);
         }
         __syncthreads();
         const bool complete = cw.ja == 0 && cw.jb == cw.r.n;
         const uint64_t u0 = pre[cw.b] + (uint64_t)cw.row * cw.r.n;  // the row's first unit
         float* const parts = reinterpret_cast<float*>(p.ws + 64 + ATTN_MAX_CTAS);
-        auto store = [&](int c, float (&y)[4], float M, float L) {
+        auto store = [&](int c, float (&y)[4], float mx, float L) {
             const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] *= inv;
@@ -573,29 +703,29 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
             const T h[4] = {from_f32<DT>(y[0]), from_f32<DT>(y[1]), from_f32<DT>(y[2]), from_f32<DT>(y[3])};
             *reinterpret_cast<uint2*>(out + 4 * lane) = *reinterpret_cast<const uint2*>(h);
             if (p.lse && lane == 0)
-                p.lse[row * ((int64_t)p.Hkv * p.group) + hq_] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+                p.lse[row * ((int64_t)p.Hkv * p.group) + hq_] = L > 0.0f ? (mx + log2f(L)) * 0.6931471805599453f : -INFINITY;
         };
         // partial results: CTA c's slot 0 for a row that began before it, slot 1 for one that goes on after it
         float* const mine = parts + (size_t)(2 * blockIdx.x + (cw.ja == 0 ? 1 : 0)) * ATTN_PART;
         for (int c = w; c < tile_cols; c += W) {
-            float M = ATTN_NONE, L = 0.0f, y[4] = {};
+            float mx = ATTN_NONE, L = 0.0f, y[4] = {};
 #pragma unroll
-            for (int k = 0; k < W; ++k) M = fmaxf(M, sh.m[k][c]);
+            for (int k = 0; k < W; ++k) mx = fmaxf(mx, sh.m[k][c]);
 #pragma unroll
-            for (int k = 0; k < W; ++k) {
-                const float f = ex2(sh.m[k][c] - M);
+            for (int k = 0; k < W; ++k) L += ex2(sh.m[k][c] - mx) * sh.l[k][c];
+#pragma unroll
+            for (int k = 0; k < W / 2; ++k) {
                 const float4 v = *reinterpret_cast<const float4*>(&sh.o[k][c][4 * lane]);
-                L += f * sh.l[k][c];
-                y[0] += f * v.x;
-                y[1] += f * v.y;
-                y[2] += f * v.z;
-                y[3] += f * v.w;
+                y[0] += v.x;
+                y[1] += v.y;
+                y[2] += v.z;
+                y[3] += v.w;
             }
             if (complete) {
-                store(c, y, M, L);
+                store(c, y, mx, L);
             } else {
                 __stcg(reinterpret_cast<float4*>(mine + c * 128 + 4 * lane), make_float4(y[0], y[1], y[2], y[3]));
-                if (lane == 0) __stcg(reinterpret_cast<float2*>(mine + ATTN_MAX_NC * 128 + 2 * c), make_float2(M, L));
+                if (lane == 0) __stcg(reinterpret_cast<float2*>(mine + ATTN_MAX_NC * 128 + 2 * c), make_float2(mx, L));
             }
         }
         if (!complete) {
@@ -612,24 +742,30 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
             if (sh.last) {
                 __threadfence();
                 for (int c = w; c < tile_cols; c += W) {
-                    float M = ATTN_NONE, L = 0.0f, y[4] = {};
+                    float mx = ATTN_NONE, L = 0.0f, y[4] = {};
                     for (uint32_t k = first; k <= last; ++k) {
                         const float* part = parts + (size_t)(2 * k + (k == first ? 1 : 0)) * ATTN_PART;
                         const float2 ml = __ldcg(reinterpret_cast<const float2*>(part + ATTN_MAX_NC * 128 + 2 * c));
                         const float4 v = __ldcg(reinterpret_cast<const float4*>(part + c * 128 + 4 * lane));
-                        const float t = fmaxf(M, ml.x), fa = ex2(M - t), fb = ex2(ml.x - t);
-                        M = t;
+                        const float t = fmaxf(mx, ml.x), fa = ex2(mx - t), fb = ex2(ml.x - t);
+                        mx = t;
                         L = L * fa + ml.y * fb;
                         y[0] = y[0] * fa + v.x * fb;
                         y[1] = y[1] * fa + v.y * fb;
                         y[2] = y[2] * fa + v.z * fb;
                         y[3] = y[3] * fa + v.w * fb;
                     }
-                    store(c, y, M, L);
+                    store(c, y, mx, L);
                 }
             }
         }
-        __syncthreads();  // the merge buffer and q are free again
+        __syncthreads();  // the merge buffer, q and the piece's record are free again
+        if (tid == 0) {
+            Walk t = cw;
+            walk_next(p, pre, NC, us, t);
+            cw = t;
+        }
+        __syncthreads();
     }
 }
 

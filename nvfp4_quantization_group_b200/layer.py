@@ -47,25 +47,37 @@ SIGNATURES = {
 }
 
 
-def _need(ok: bool, status: int, what: str) -> None:
+def _need(ok: bool, status: int, *what: str) -> None:
     if not ok:
-        raise HQError(status, what)
+        raise HQError(status, ": ".join(what))
 
 
-def _same_device(what: str, first: torch.Tensor, *others) -> torch.device:
-    _need(first.is_cuda, HQ_ERR_UNSUPPORTED, what + ": a CUDA tensor is needed")
+# handle of a device's current stream (the direct call saves a microsecond of building a Stream object)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+
+
+def _ptr(t) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def _device(what: str, first: torch.Tensor, *others) -> int:
+    """Index of the CUDA device that all tensors are on."""
+    d = first.get_device()
+    if d < 0:
+        raise HQError(HQ_ERR_UNSUPPORTED, what + ": a CUDA tensor is needed")
     for t in others:
-        _need(t is None or t.device == first.device, HQ_ERR_UNSUPPORTED, what + ": tensors on different devices")
-    return first.device
+        if t is not None and t.get_device() != d:
+            raise HQError(HQ_ERR_UNSUPPORTED, what + ": tensors on different devices")
+    return d
 
 
-def _launch(device: torch.device, stream, inputs, call):
+def _launch(device: int, stream, inputs, call):
     """call(stream handle) with `device` current, allocations on the stream that the work goes to."""
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            return call(torch.cuda.current_stream(device).cuda_stream)
+        if device == torch.cuda.current_device():
+            return call(_raw_stream(device))
         with torch.cuda.device(device):
-            return call(torch.cuda.current_stream(device).cuda_stream)
+            return call(_raw_stream(device))
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device)
     with torch.cuda.device(device), torch.cuda.stream(s):
         for t in inputs:
@@ -96,18 +108,23 @@ def hq_rmsnorm_backward(dtype, dy, dy_row_stride, h, h_row_stride, weight, w_dty
                                      _stream(stream)), "hq_rmsnorm_backward")
 
 
-def _rows(what: str, name: str, t: torch.Tensor, like: torch.Tensor) -> int:
-    """Row stride of a [M, K] tensor of `like`'s type and shape with contiguous rows."""
-    _need(t.shape == like.shape, HQ_ERR_SHAPE, f"{what}: {name}'s shape")
-    _need(t.dtype == like.dtype, HQ_ERR_UNSUPPORTED, f"{what}: {name}'s type")
-    _need(t.stride(1) == 1, HQ_ERR_ALIGN, f"{what}: {name}'s rows are not contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _rows(what: str, name: str, t: torch.Tensor, shape, dtype) -> int:
+    """Row stride of a tensor of the given [M, K] and type with contiguous rows."""
+    if t.shape != shape:
+        raise HQError(HQ_ERR_SHAPE, f"{what}: {name}'s shape")
+    if t.dtype != dtype:
+        raise HQError(HQ_ERR_UNSUPPORTED, f"{what}: {name}'s type")
+    row, one = t.stride()
+    if one != 1:
+        raise HQError(HQ_ERR_ALIGN, f"{what}: {name}'s rows are not contiguous")
+    return row if shape[0] > 1 else shape[1]
 
 
-def _weight(what: str, w: torch.Tensor, x: torch.Tensor) -> int:
-    _need(w.shape == (x.shape[1],) and w.is_contiguous(), HQ_ERR_SHAPE, what + ": weight's shape")
-    _need(w.dtype == x.dtype or w.dtype == torch.float32, HQ_ERR_UNSUPPORTED, what + ": weight's type")
-    return _DTYPE[w.dtype]
+def _weight(what: str, w: torch.Tensor, K: int, dtype) -> int:
+    _need(w.shape == (K,) and w.is_contiguous(), HQ_ERR_SHAPE, what, "weight's shape")
+    t = w.dtype
+    _need(t == dtype or t == torch.float32, HQ_ERR_UNSUPPORTED, what, "weight's type")
+    return _DTYPE[t]
 
 
 def add_rmsnorm_fp8_k128(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
@@ -117,34 +134,38 @@ def add_rmsnorm_fp8_k128(x: torch.Tensor, weight: torch.Tensor, residual: torch.
     residual_out (with a residual: what the norm read; into `residual_out` where given, which may be x or residual
     itself) and, when asked, rstd [M] and amax."""
     what = "add_rmsnorm_fp8_k128"
-    _need(x.dim() == 2, HQ_ERR_SHAPE, what + ": x is [M, K]")
-    _need(x.dtype in _DTYPE, HQ_ERR_UNSUPPORTED, what + ": x's type")
-    dev = _same_device(what, x, weight, residual, residual_out)
-    M, K = x.shape
-    xs, rs = _rows(what, "x", x, x), 0 if residual is None else _rows(what, "residual", residual, x)
-    wd = _weight(what, weight, x)
+    shape, dtype = x.shape, x.dtype
+    _need(len(shape) == 2, HQ_ERR_SHAPE, what, "x is [M, K]")
+    _need(dtype in _DTYPE, HQ_ERR_UNSUPPORTED, what, "x's type")
+    dev = _device(what, x, weight, residual, residual_out)
+    M, K = shape
+    xs, rs = _rows(what, "x", x, shape, dtype), 0 if residual is None else _rows(what, "residual", residual, shape, dtype)
+    wd = _weight(what, weight, K, dtype)
     if residual_out is not None:
-        _need(residual is not None, HQ_ERR_NULL, what + ": residual_out without a residual")
-        _rows(what, "residual_out", residual_out, x)
-        _need(residual_out.is_contiguous(), HQ_ERR_ALIGN, what + ": residual_out is not contiguous")
+        _need(residual is not None, HQ_ERR_NULL, what, "residual_out without a residual")
+        _rows(what, "residual_out", residual_out, shape, dtype)
+        _need(residual_out.is_contiguous(), HQ_ERR_ALIGN, what, "residual_out is not contiguous")
     groups = K // 128
 
     def call(s):
-        out = {"codes": torch.empty((M, K), dtype=torch.uint8, device=dev)}
+        out = {"codes": x.new_empty(shape, dtype=torch.uint8)}
         if (scale_layout & ~HQ_FP8_UE8M0) == HQ_SCALE_TRANSPOSED:
             ld = M if scale_ld is None else scale_ld
-            out["scales"] = torch.empty((groups, ld), dtype=torch.float32, device=dev)
+            scales = x.new_empty((groups, ld), dtype=torch.float32)
         else:
             ld = groups
-            out["scales"] = torch.empty((M, groups), dtype=torch.float32, device=dev)
+            scales = x.new_empty((M, groups), dtype=torch.float32)
+        out["scales"] = scales
         if residual is not None:
-            out["residual_out"] = torch.empty((M, K), dtype=x.dtype, device=dev) if residual_out is None else residual_out
+            out["residual_out"] = x.new_empty(shape) if residual_out is None else residual_out
         if want_rstd:
-            out["rstd"] = torch.empty(M, dtype=torch.float32, device=dev)
+            out["rstd"] = x.new_empty((M,), dtype=torch.float32)
         if want_amax:
-            out["amax"] = torch.empty_like(out["scales"])
-        hq_add_rmsnorm_fp8_k128(_DTYPE[x.dtype], x, xs, residual, rs, weight, wd, eps, M, K, out.get("residual_out"),
-                                out["codes"], out["scales"], scale_layout, ld, out.get("rstd"), out.get("amax"), s)
+            out["amax"] = torch.empty_like(scales)
+        _check(lib().hq_add_rmsnorm_fp8_k128(
+            _DTYPE[dtype], x.data_ptr(), xs, _ptr(residual), rs, weight.data_ptr(), wd, eps, M, K,
+            _ptr(out.get("residual_out")), out["codes"].data_ptr(), scales.data_ptr(), scale_layout, ld,
+            _ptr(out.get("rstd")), _ptr(out.get("amax")), s), what)
         return out
 
     return _launch(dev, stream, (x, weight, residual, residual_out), call)
@@ -164,27 +185,42 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rs
     without a residual), dres the gradient that reaches h along the residual -> (dx [M, K], dweight FP32 [K] or None).
     dx is written into `dx` where given (it may be dy or dres itself)."""
     what = "rmsnorm_backward"
-    _need(dy.dim() == 2, HQ_ERR_SHAPE, what + ": dy is [M, K]")
-    _need(dy.dtype in _DTYPE, HQ_ERR_UNSUPPORTED, what + ": dy's type")
-    dev = _same_device(what, dy, h, weight, rstd, dres, ws, dx)
-    M, K = dy.shape
-    gs, hs = _rows(what, "dy", dy, dy), _rows(what, "h", h, dy)
-    rs = 0 if dres is None else _rows(what, "dres", dres, dy)
-    wd = _weight(what, weight, dy)
-    _need(rstd.shape == (M,) and rstd.is_contiguous(), HQ_ERR_SHAPE, what + ": rstd's shape")
-    _need(rstd.dtype == torch.float32, HQ_ERR_UNSUPPORTED, what + ": rstd's type")
+    shape, dtype = dy.shape, dy.dtype
+    _need(len(shape) == 2, HQ_ERR_SHAPE, what, "dy is [M, K]")
+    _need(dtype in _DTYPE, HQ_ERR_UNSUPPORTED, what, "dy's type")
+    dev = _device(what, dy, h, weight, rstd, dres, ws, dx)
+    M, K = shape
+    gs, hs = _rows(what, "dy", dy, shape, dtype), _rows(what, "h", h, shape, dtype)
+    rs = 0 if dres is None else _rows(what, "dres", dres, shape, dtype)
+    wd = _weight(what, weight, K, dtype)
+    _need(rstd.shape == (M,) and rstd.is_contiguous(), HQ_ERR_SHAPE, what, "rstd's shape")
+    _need(rstd.dtype == torch.float32, HQ_ERR_UNSUPPORTED, what, "rstd's type")
     if dx is not None:
-        _rows(what, "dx", dx, dy)
-        _need(dx.is_contiguous(), HQ_ERR_ALIGN, what + ": dx is not contiguous")
+        _rows(what, "dx", dx, shape, dtype)
+        _need(dx.is_contiguous(), HQ_ERR_ALIGN, what, "dx is not contiguous")
 
     def call(s):
-        out = torch.empty((M, K), dtype=dy.dtype, device=dev) if dx is None else dx
-        dw = torch.empty(K, dtype=torch.float32, device=dev) if want_dweight else None
-        w = rmsnorm_backward_workspace(M, K, dev) if want_dweight and ws is None else ws
-        hq_rmsnorm_backward(_DTYPE[dy.dtype], dy, gs, h, hs, weight, wd, rstd, dres, rs, M, K, out, dw, w, s)
+        out = dy.new_empty(shape) if dx is None else dx
+        dw = dy.new_empty((K,), dtype=torch.float32) if want_dweight else None
+        w = rmsnorm_backward_workspace(M, K, dy.device) if want_dweight and ws is None else ws
+        _check(lib().hq_rmsnorm_backward(
+            _DTYPE[dtype], dy.data_ptr(), gs, h.data_ptr(), hs, weight.data_ptr(), wd, rstd.data_ptr(), _ptr(dres), rs, M,
+            K, out.data_ptr(), _ptr(dw), _ptr(w), 0 if w is None else w.nbytes, s), what)
         return out, dw
 
     return _launch(dev, stream, (dy, h, weight, rstd, dres, ws, dx), call)
+
+
+def _heads(what: str, name: str, t: torch.Tensor, shape, dtype):
+    """Token and head strides of a [T, heads, D] tensor of the given shape and type with contiguous rows."""
+    if t.shape != shape:
+        raise HQError(HQ_ERR_SHAPE, f"{what}: {name}'s shape")
+    if t.dtype != dtype:
+        raise HQError(HQ_ERR_UNSUPPORTED, f"{what}: {name}'s type")
+    token, head, one = t.stride()
+    if one != 1 and shape[2] > 1:
+        raise HQError(HQ_ERR_ALIGN, f"{what}: {name}'s rows are not contiguous")
+    return token, head
 
 
 # ------------------------------------------------------------------- rope
@@ -222,32 +258,31 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_f
     unless given (q and k themselves: in place).  The rotated part is 2 * len(inv_freq) wide, from dimension `offset`;
     inverse=True is the gradient with respect to the inputs."""
     what = "rope"
-    _need(q.dim() == 3, HQ_ERR_SHAPE, what + ": q is [T, heads, D]")
-    _need(q.dtype in _DTYPE, HQ_ERR_UNSUPPORTED, what + ": q's type")
-    dev = _same_device(what, q, k, positions, inv_freq, q_out, k_out)
-    T, Hq, D = q.shape
-    for name, t, like in (("q", q, q), ("k", k, None if k is None else k), ("q_out", q_out, q), ("k_out", k_out, k)):
-        if t is None:
-            continue
-        _need(like is not None and t.shape == like.shape and t.dim() == 3 and t.shape[0] == T and t.shape[2] == D,
-              HQ_ERR_SHAPE, f"{what}: {name}'s shape")
-        _need(t.dtype == q.dtype, HQ_ERR_UNSUPPORTED, f"{what}: {name}'s type")
-        _need(D <= 1 or t.stride(2) == 1, HQ_ERR_ALIGN, f"{what}: {name}'s rows are not contiguous")
-    _need(positions.shape == (T,) and positions.is_contiguous(), HQ_ERR_SHAPE, what + ": positions' shape")
-    _need(positions.dtype == torch.int64, HQ_ERR_UNSUPPORTED, what + ": positions' type")
-    _need(inv_freq.dim() == 1 and inv_freq.is_contiguous(), HQ_ERR_SHAPE, what + ": inv_freq's shape")
-    _need(inv_freq.dtype == torch.float64, HQ_ERR_UNSUPPORTED, what + ": inv_freq's type")
-    Hk = 0 if k is None else k.shape[1]
+    shape, dtype = q.shape, q.dtype
+    _need(len(shape) == 3, HQ_ERR_SHAPE, what, "q is [T, heads, D]")
+    _need(dtype in _DTYPE, HQ_ERR_UNSUPPORTED, what, "q's type")
+    dev = _device(what, q, k, positions, inv_freq, q_out, k_out)
+    T, Hq, D = shape
+    qs = _heads(what, "q", q, shape, dtype)
+    kshape, ks, Hk = None, (0, 0), 0
+    if k is not None:
+        kshape = k.shape
+        _need(len(kshape) == 3 and kshape[0] == T and kshape[2] == D, HQ_ERR_SHAPE, what, "k's shape")
+        ks, Hk = _heads(what, "k", k, kshape, dtype), kshape[1]
+    _need(k is not None or k_out is None, HQ_ERR_SHAPE, what, "k_out without k")
+    _need(positions.shape == (T,) and positions.is_contiguous(), HQ_ERR_SHAPE, what, "positions' shape")
+    _need(positions.dtype == torch.int64, HQ_ERR_UNSUPPORTED, what, "positions' type")
+    _need(inv_freq.dim() == 1 and inv_freq.is_contiguous(), HQ_ERR_SHAPE, what, "inv_freq's shape")
+    _need(inv_freq.dtype == torch.float64, HQ_ERR_UNSUPPORTED, what, "inv_freq's type")
+    qos = (Hq * D, D) if q_out is None else _heads(what, "q_out", q_out, shape, dtype)
+    kos = (Hk * D, D) if k_out is None else _heads(what, "k_out", k_out, kshape, dtype)
 
     def call(s):
-        qo = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if q_out is None else q_out
-        ko = k_out
-        if k is not None and ko is None:
-            ko = torch.empty((T, Hk, D), dtype=q.dtype, device=dev)
-        ks, kos = (0, 0) if k is None else (k.stride(0), k.stride(1)), (0, 0) if k is None else (ko.stride(0), ko.stride(1))
-        hq_rope(_DTYPE[q.dtype], q, q.stride(0), q.stride(1), Hq, k, ks[0], ks[1], Hk, T, D, positions, inv_freq,
-                2 * inv_freq.shape[0], offset, layout, magnitude, bool(inverse), qo, qo.stride(0), qo.stride(1), ko,
-                kos[0], kos[1], s)
+        qo = q.new_empty(shape) if q_out is None else q_out
+        ko = k.new_empty(kshape) if k is not None and k_out is None else k_out
+        _check(lib().hq_rope(_DTYPE[dtype], q.data_ptr(), qs[0], qs[1], Hq, _ptr(k), ks[0], ks[1], Hk, T, D,
+                             positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0], offset, layout, magnitude,
+                             1 if inverse else 0, qo.data_ptr(), qos[0], qos[1], _ptr(ko), kos[0], kos[1], s), what)
         return qo, ko
 
     return _launch(dev, stream, (q, k, positions, inv_freq, q_out, k_out), call)
@@ -268,27 +303,32 @@ def kv_slots(lens: torch.Tensor, new_tokens: torch.Tensor, block_table: torch.Te
     of new tensors lens, cu_new, slots, positions, free_count, status.  Pass lens_out=lens and
     free_count_out=free_count to update those in place too."""
     what = "kv_slots"
-    dev = _same_device(what, lens, new_tokens, block_table, free_pages, free_count, lens_out, free_count_out)
+    dev = _device(what, lens, new_tokens, block_table, free_pages, free_count, lens_out, free_count_out)
     B = lens.shape[0] if lens.dim() == 1 else -1
-    for name, t, shape in (("lens", lens, (B,)), ("new_tokens", new_tokens, (B,)), ("free_count", free_count, (1,)),
-                           ("lens_out", lens_out, (B,)), ("free_count_out", free_count_out, (1,)),
-                           ("free_pages", free_pages, (free_pages.numel(),)),
-                           ("block_table", block_table, (B, block_table.shape[-1] if block_table.dim() else 0))):
+    width = block_table.shape[-1] if block_table.dim() == 2 else -1
+    for name, t, shape in (("lens", lens, (B,)), ("new_tokens", new_tokens, (B,)), ("block_table", block_table, (B, width)),
+                           ("free_pages", free_pages, (free_pages.numel(),)), ("free_count", free_count, (1,)),
+                           ("lens_out", lens_out, (B,)), ("free_count_out", free_count_out, (1,))):
         if t is None:
             continue
-        _need(t.shape == shape and t.is_contiguous(), HQ_ERR_SHAPE, f"{what}: {name}'s shape")
-        _need(t.dtype == torch.int32, HQ_ERR_UNSUPPORTED, f"{what}: {name}'s type")
+        if t.shape != shape or not t.is_contiguous():
+            raise HQError(HQ_ERR_SHAPE, f"{what}: {name}'s shape")
+        if t.dtype != torch.int32:
+            raise HQError(HQ_ERR_UNSUPPORTED, f"{what}: {name}'s type")
+    _need(n_slots >= 0, HQ_ERR_SHAPE, what, "n_slots")
 
     def call(s):
-        i32, i64 = dict(dtype=torch.int32, device=dev), dict(dtype=torch.int64, device=dev)
-        out = {"lens": torch.empty(B, **i32) if lens_out is None else lens_out, "cu_new": torch.empty(B + 1, **i32),
-               "slots": torch.empty(n_slots, **i64), "positions": torch.empty(n_slots, **i64),
-               "free_count": torch.empty(1, **i32) if free_count_out is None else free_count_out,
-               "status": torch.empty(1, **i32)}
-        hq_kv_slots(B, lens, new_tokens, block_table, block_table.shape[1], free_pages, free_pages.numel(), free_count,
-                    page_size, n_slots, out["lens"], out["cu_new"], out["slots"], out["positions"], out["free_count"],
-                    out["status"], s)
-        return out
+        lo, cu, count, status = lens.new_empty((2 * B + 3,)).split((B, B + 1, 1, 1))
+        if lens_out is not None:
+            lo = lens_out
+        if free_count_out is not None:
+            count = free_count_out
+        slots, positions = lens.new_empty((2, n_slots), dtype=torch.int64).unbind()
+        _check(lib().hq_kv_slots(B, lens.data_ptr(), new_tokens.data_ptr(), block_table.data_ptr(), width,
+                                 free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(), page_size, n_slots,
+                                 lo.data_ptr(), cu.data_ptr(), slots.data_ptr(), positions.data_ptr(), count.data_ptr(),
+                                 status.data_ptr(), s), what)
+        return {"lens": lo, "cu_new": cu, "slots": slots, "positions": positions, "free_count": count, "status": status}
 
     return _launch(dev, stream, (lens, new_tokens, block_table, free_pages, free_count, lens_out, free_count_out), call)
 
@@ -306,10 +346,11 @@ def kv4_cache(num_pages: int, page_size: int, H: int, device="cuda") -> torch.Te
 
 def _cache_shape(what: str, cache: torch.Tensor):
     """(pages, page_size, heads) of a cache."""
-    _need(cache.dim() == 4 and cache.shape[3] == HQ_KV4_GROUP_BYTES and cache.is_contiguous(), HQ_ERR_SHAPE,
-          what + ": the cache is [pages, heads, page_size / 16, 2432], contiguous")
-    _need(cache.dtype == torch.uint8, HQ_ERR_UNSUPPORTED, what + ": the cache's type")
-    return cache.shape[0], cache.shape[2] * HQ_KV4_GROUP_TOKENS, cache.shape[1]
+    shape = cache.shape
+    _need(len(shape) == 4 and shape[3] == HQ_KV4_GROUP_BYTES and cache.is_contiguous(), HQ_ERR_SHAPE, what,
+          "the cache is [pages, heads, page_size / 16, 2432], contiguous")
+    _need(cache.dtype == torch.uint8, HQ_ERR_UNSUPPORTED, what, "the cache's type")
+    return shape[0], shape[2] * HQ_KV4_GROUP_TOKENS, shape[1]
 
 
 def hq_kv4_append(dtype, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, slots, N, H, hadamard_n,
@@ -327,8 +368,8 @@ def hq_kv4_gather(dtype, cache, num_pages, page_size, slots, N, H, hadamard_n, k
 
 
 def _slots_arg(what: str, slots: torch.Tensor) -> int:
-    _need(slots.dim() == 1 and slots.is_contiguous(), HQ_ERR_SHAPE, what + ": slots' shape")
-    _need(slots.dtype == torch.int64, HQ_ERR_UNSUPPORTED, what + ": slots' type")
+    _need(slots.dim() == 1 and slots.is_contiguous(), HQ_ERR_SHAPE, what, "slots' shape")
+    _need(slots.dtype == torch.int64, HQ_ERR_UNSUPPORTED, what, "slots' type")
     return slots.shape[0]
 
 
@@ -336,17 +377,15 @@ def kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: tor
                stream=None) -> None:
     """Quantize keys and values [N, H, 128] into the cache's slots (see hq.h); slots outside the cache are skipped."""
     what = "kv4_append"
-    dev = _same_device(what, cache, k, v, slots)
+    dev = _device(what, cache, k, v, slots)
     pages, page, H = _cache_shape(what, cache)
-    N = _slots_arg(what, slots)
-    for name, t in (("k", k), ("v", v)):
-        _need(t.shape == (N, H, HQ_KV4_HEAD), HQ_ERR_SHAPE, f"{what}: {name}'s shape")
-        _need(t.dtype == k.dtype and t.dtype in _DTYPE, HQ_ERR_UNSUPPORTED, f"{what}: {name}'s type")
-        _need(t.stride(2) == 1, HQ_ERR_ALIGN, f"{what}: {name}'s rows are not contiguous")
+    N, dtype = _slots_arg(what, slots), k.dtype
+    _need(dtype in _DTYPE, HQ_ERR_UNSUPPORTED, what, "k's type")
+    (kt, kh), (vt, vh) = (_heads(what, n, t, (N, H, HQ_KV4_HEAD), dtype) for n, t in (("k", k), ("v", v)))
 
     def call(s):
-        hq_kv4_append(_DTYPE[k.dtype], k, k.stride(0), k.stride(1), v, v.stride(0), v.stride(1), slots, N, H, hadamard_n,
-                      cache, pages, page, s)
+        _check(lib().hq_kv4_append(_DTYPE[dtype], k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(), N, H,
+                                   hadamard_n, cache.data_ptr(), pages, page, s), what)
 
     _launch(dev, stream, (k, v, slots, cache), call)
 
@@ -355,16 +394,16 @@ def kv4_gather(cache: torch.Tensor, slots: torch.Tensor, dtype: torch.dtype = to
                stream=None):
     """Keys and values [N, H, 128] of the cache's slots (see hq.h), rotated back with hadamard_n 128 -> (k, v)."""
     what = "kv4_gather"
-    dev = _same_device(what, cache, slots)
+    dev = _device(what, cache, slots)
     pages, page, H = _cache_shape(what, cache)
     N = _slots_arg(what, slots)
-    _need(dtype in _DTYPE, HQ_ERR_UNSUPPORTED, what + ": dtype")
+    _need(dtype in _DTYPE, HQ_ERR_UNSUPPORTED, what, "dtype")
 
     def call(s):
-        k = torch.empty((N, H, HQ_KV4_HEAD), dtype=dtype, device=dev)
-        v = torch.empty_like(k)
-        hq_kv4_gather(_DTYPE[dtype], cache, pages, page, slots, N, H, hadamard_n, k, k.stride(0), k.stride(1), v,
-                      v.stride(0), v.stride(1), s)
+        k, v = cache.new_empty((2, N, H, HQ_KV4_HEAD), dtype=dtype).unbind()
+        t = H * HQ_KV4_HEAD
+        _check(lib().hq_kv4_gather(_DTYPE[dtype], cache.data_ptr(), pages, page, slots.data_ptr(), N, H, hadamard_n,
+                                   k.data_ptr(), t, HQ_KV4_HEAD, v.data_ptr(), t, HQ_KV4_HEAD, s), what)
         return k, v
 
     return _launch(dev, stream, (cache, slots), call)
@@ -389,7 +428,7 @@ def hq_kv4_attention(dtype, q, q_token_stride, q_head_stride, Tq, Hq, cache, num
 def kv4_attention_workspace(device="cuda", stream=None) -> torch.Tensor:
     """A workspace of kv4_attention in its rest state; for any shapes, one call at a time."""
     ws = torch.empty(hq_kv4_attention_workspace_size(), dtype=torch.uint8, device=device)
-    _launch(ws.device, stream, (ws,), lambda s: hq_workspace_init(ws, s))
+    _launch(_device("kv4_attention_workspace", ws), stream, (ws,), lambda s: hq_workspace_init(ws, s))
     return ws
 
 
@@ -401,32 +440,32 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     [Tq, Hq]) with want_lse.  Rows behind the last request's are left as they were (uninitialized in a new tensor).
     scale: 1 / sqrt(128) unless given."""
     what = "kv4_attention"
-    dev = _same_device(what, q, cache, block_table, seq_lens, cu_q, ws, out)
+    dev = _device(what, q, cache, block_table, seq_lens, cu_q, ws, out)
     pages, page, Hkv = _cache_shape(what, cache)
-    _need(q.dim() == 3 and q.shape[2] == HQ_KV4_HEAD, HQ_ERR_SHAPE, what + ": q is [Tq, heads, 128]")
-    _need(q.dtype in (torch.bfloat16, torch.float16), HQ_ERR_UNSUPPORTED, what + ": q's type")
-    _need(q.stride(2) == 1, HQ_ERR_ALIGN, what + ": q's rows are not contiguous")
-    Tq, Hq, _ = q.shape
+    shape, dtype = q.shape, q.dtype
+    _need(len(shape) == 3 and shape[2] == HQ_KV4_HEAD, HQ_ERR_SHAPE, what, "q is [Tq, heads, 128]")
+    _need(dtype == torch.bfloat16 or dtype == torch.float16, HQ_ERR_UNSUPPORTED, what, "q's type")
+    Tq, Hq, _ = shape
+    qs = _heads(what, "q", q, shape, dtype)
+    os = (Hq * HQ_KV4_HEAD, HQ_KV4_HEAD) if out is None else _heads(what, "out", out, shape, dtype)
     B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
-    _need(block_table.dim() == 2 and block_table.shape[0] == B and block_table.is_contiguous(), HQ_ERR_SHAPE,
-          what + ": block_table's shape")
-    for name, t, n in (("seq_lens", seq_lens, B), ("cu_q", cu_q, B + 1)):
-        if t is not None:
-            _need(t.shape == (n,) and t.is_contiguous(), HQ_ERR_SHAPE, f"{what}: {name}'s shape")
-            _need(t.dtype == torch.int32, HQ_ERR_UNSUPPORTED, f"{what}: {name}'s type")
-    _need(block_table.dtype == torch.int32, HQ_ERR_UNSUPPORTED, what + ": block_table's type")
-    if out is not None:
-        _need(out.shape == q.shape, HQ_ERR_SHAPE, what + ": out's shape")
-        _need(out.dtype == q.dtype, HQ_ERR_UNSUPPORTED, what + ": out's type")
-        _need(out.stride(2) == 1, HQ_ERR_ALIGN, what + ": out's rows are not contiguous")
+    width = block_table.shape[-1] if block_table.dim() == 2 else -1
+    for name, t, n in (("block_table", block_table, (B, width)), ("seq_lens", seq_lens, (B,)), ("cu_q", cu_q, (B + 1,))):
+        if t is None:
+            continue
+        if t.shape != n or not t.is_contiguous():
+            raise HQError(HQ_ERR_SHAPE, f"{what}: {name}'s shape")
+        if t.dtype != torch.int32:
+            raise HQError(HQ_ERR_UNSUPPORTED, f"{what}: {name}'s type")
 
     def call(s):
-        o = torch.empty((Tq, Hq, HQ_KV4_HEAD), dtype=q.dtype, device=dev) if out is None else out
-        lse = torch.empty((Tq, Hq), dtype=torch.float32, device=dev) if want_lse else None
-        w = kv4_attention_workspace(dev) if ws is None else ws
-        hq_kv4_attention(_DTYPE[q.dtype], q, q.stride(0), q.stride(1), Tq, Hq, cache, pages, page, Hkv, block_table,
-                         block_table.shape[1], B, seq_lens, cu_q, q_len, HQ_KV4_HEAD ** -0.5 if scale is None else scale,
-                         window, sinks, hadamard_n, o, o.stride(0), o.stride(1), lse, w, s)
+        o = q.new_empty(shape) if out is None else out
+        lse = q.new_empty((Tq, Hq), dtype=torch.float32) if want_lse else None
+        w = kv4_attention_workspace(q.device) if ws is None else ws
+        _check(lib().hq_kv4_attention(_DTYPE[dtype], q.data_ptr(), qs[0], qs[1], Tq, Hq, cache.data_ptr(), pages, page, Hkv,
+                                      block_table.data_ptr(), width, B, seq_lens.data_ptr(), _ptr(cu_q), q_len,
+                                      HQ_KV4_HEAD ** -0.5 if scale is None else scale, window, sinks, hadamard_n,
+                                      o.data_ptr(), os[0], os[1], _ptr(lse), w.data_ptr(), w.nbytes, s), what)
         return (o, lse) if want_lse else o
 
     return _launch(dev, stream, (q, cache, block_table, seq_lens, cu_q, ws, out), call)
