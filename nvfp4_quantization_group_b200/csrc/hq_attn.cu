@@ -29,13 +29,11 @@
 
 namespace hq {
 
-#ifndef HQ_ATTN_FEW
-#define HQ_ATTN_FEW 2
-#endif
-#ifndef HQ_ATTN_STAGES
-#define HQ_ATTN_STAGES 2
-#endif
-constexpr int ATTN_STAGES = HQ_ATTN_STAGES;  // units in flight per warp
+constexpr int ATTN_STAGES = 2;       // units in flight per warp
+// Units that a row's start and end (its q, the joins) are worth: 48 requests
+// with a window of 2047 tokens and up to 20 columns take 55 us with 4, 48 with
+// 8, 45 with 12 or 16, 47 with 24.
+constexpr int ATTN_ROW_COST = 16;
 constexpr int ATTN_MAX_CTAS = 1024;  // workspace: CTAs of a launch at most
 constexpr int ATTN_MAX_NC = 16;
 constexpr int ATTN_PART = ATTN_MAX_NC * (128 + 2);  // floats of one partial result
@@ -43,8 +41,11 @@ constexpr float ATTN_NONE = -1e30f;  // running maximum before any token
 
 // ---------------------------------------------------------------- schedule
 // Units of one or two groups (16 << us tokens, us = 0 or 1) are numbered request by request, then (head, column
-// tile) row by row, then in the order of the tokens.  CTA c of G takes units
-// [U c / G, U (c + 1) / G): the same load for every CTA whatever the lengths.
+// tile) row by row, then in the order of the tokens.  Each row counts
+// ATTN_ROW_COST units more than it has, in front of them: what starting and
+// ending a row costs.  CTA c of G takes units [U c / G, U (c + 1) / G), a cut
+// in a row's front part (or right behind it) moved to the row's start: about the same load for every
+// CTA whatever the lengths.
 struct Request {
     int q0, nq;       // first row of q, query tokens
     int len;          // tokens (clamped to the block table's row)
@@ -52,7 +53,7 @@ struct Request {
     int tiles;        // column tiles
     int sink_units;   // units of the first tokens, before the window's
     int first_unit;   // the window's first unit
-    int n;            // units per row (at least 1 where there are queries)
+    int n;            // units per row, ATTN_ROW_COST among them (no tokens: one more)
     bool bad;         // the length exceeds the block table's row
 };
 
@@ -75,7 +76,7 @@ __device__ __forceinline__ Request attn_request(const AttnParams& p, int b, int 
     const int lo = p.window > 0 && first > 0 ? (int)min(first, (int64_t)r.len) : 0;
     r.first_unit = lo >> (4 + us);
     r.sink_units = min((min(p.sinks, lo) + ut - 1) >> (4 + us), r.first_unit);
-    r.n = r.nq ? max(1, r.sink_units + ((r.len + ut - 1) >> (4 + us)) - r.first_unit) : 0;
+    r.n = r.nq ? ATTN_ROW_COST + max(1, r.sink_units + ((r.len + ut - 1) >> (4 + us)) - r.first_unit) : 0;
     return r;
 }
 
@@ -83,7 +84,7 @@ __device__ __forceinline__ Request attn_request(const AttnParams& p, int b, int 
 struct Walk {
     Request r;
     int b, row, head;     // request, row (head, column tile) of it, the row's head
-    int ja, jb;           // units of the piece: [ja, jb) of r.n
+    int ja, jb;           // units of the piece: [ja, jb) of r.n (the first ATTN_ROW_COST have no tokens)
     uint64_t at, end;     // next unit, end of the CTA's units
     bool live;
 };
@@ -93,9 +94,27 @@ struct Sched {
     uint32_t G;
 };
 
-__device__ __forceinline__ uint64_t cta_first(const Sched& s, uint32_t c) { return s.U * c / s.G; }
-// The CTA that holds unit u.
+// The CTA that holds unit u of a row's own units.
 __device__ __forceinline__ uint32_t cta_of(const Sched& s, uint64_t u) { return (uint32_t)(((u + 1) * s.G - 1) / s.U); }
+// The request that holds unit u: pre[b] <= u < pre[b + 1].
+__device__ __forceinline__ int request_of(const AttnParams& p, const uint64_t* pre, uint64_t u) {
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid + 1] > u) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+// The first unit of CTA c (U for c == G).
+__device__ __forceinline__ uint64_t cta_first(const AttnParams& p, const uint64_t* pre, int nc, int us, const Sched& s,
+                                              uint32_t c) {
+    const uint64_t u = s.U * c / s.G;
+    if (c == s.G) return u;
+    const int b = request_of(p, pre, u);
+    const uint32_t n = (uint32_t)attn_request(p, b, nc, us).n, in = (uint32_t)((u - pre[b]) % n);
+    return in <= ATTN_ROW_COST ? u - in : u;
+}
 
 __device__ __forceinline__ void walk_piece(const uint64_t* pre, Walk& w) {
     w.live = w.at < w.end;
@@ -113,14 +132,8 @@ __device__ __forceinline__ void walk_start(const AttnParams& p, const uint64_t* 
     w.end = end;
     w.live = at < end;
     if (!w.live) return;
-    int lo = 0, hi = p.B - 1;  // the request with pre[b] <= at < pre[b + 1]
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (pre[mid + 1] > at) hi = mid;
-        else lo = mid + 1;
-    }
-    w.b = lo;
-    w.r = attn_request(p, lo, nc, us);
+    w.b = request_of(p, pre, at);
+    w.r = attn_request(p, w.b, nc, us);
     walk_piece(pre, w);
 }
 __device__ __forceinline__ void walk_next(const AttnParams& p, const uint64_t* pre, int nc, int us, Walk& w) {
@@ -220,7 +233,7 @@ template <int NT, int W> struct AttnShared {
     float m[W][NC], l[W][NC];
     float qs[NC];  // factor of a column's scores, in powers of two
     int pos[NC];   // a column's position
-    Walk cw;       // the CTA's current piece
+    Walk cw, nw;   // the CTA's current piece and the one after it
     Walk lw[W];    // the piece of each warp's next load
     uint64_t full[W][ATTN_STAGES];
     unsigned long long warp_sums[W];
@@ -428,7 +441,7 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
         }
         if (tid == 0) pre[p.B] = carry;
         sc.U = carry;
-        if (us == 1 || carry <= (uint64_t)HQ_ATTN_FEW * W * gridDim.x) break;
+        if (us == 1 || carry <= 2ull * W * gridDim.x) break;
     }
     fence_mbar_init();
     __syncthreads();
@@ -447,25 +460,44 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
     Walk& lw = sh.lw[w];
     {
         Walk t;
-        walk_start(p, pre, NC, us, cta_first(sc, blockIdx.x), cta_first(sc, blockIdx.x + 1), t);
+        walk_start(p, pre, NC, us, cta_first(p, pre, NC, us, sc, blockIdx.x), cta_first(p, pre, NC, us, sc, blockIdx.x + 1), t);
         if (tid == 0) cw = t;
         if (lane == 0) lw = t;
     }
     __syncthreads();
+    if (!cw.live) return;  // (a CTA whose units all lie in front of a row)
+    // column c of a piece's q, four elements a lane
+    constexpr int CPW = (NC + W - 1) / W;  // columns per warp
+    uint2 qraw[CPW];
+    auto load_q = [&](const Walk& k) {
+#pragma unroll
+        for (int x = 0; x < CPW; ++x) {
+            qraw[x] = make_uint2(0u, 0u);
+            const int c = w + x * W, col = (k.row - k.head * k.r.tiles) * NC + c;
+            if (c < NC && col < k.r.nq * p.group) {
+                const int j = col / p.group, hh = col - j * p.group;
+                const T* q = static_cast<const T*>(p.q) + (int64_t)(k.r.q0 + j) * p.q_ts + (int64_t)(k.head * p.group + hh) * p.q_hs;
+                qraw[x] = *reinterpret_cast<const uint2*>(q + 4 * lane);
+            }
+        }
+    };
+    load_q(cw);
     const int groups_shift = p.page_shift - 4;
     const bool small_pages = groups_shift == 0;  // a unit's two groups lie on two pages
-    int lj = lw.ja + w;       // next unit to load of lw's piece
+    auto own = [](const Walk& k) { return max(k.ja, ATTN_ROW_COST); };
+    int lj = own(lw) + w;     // next unit to load of lw's piece
     int pg[2] = {-1, -1};     // the pages of its groups (looked up one unit ahead), or -1
     uint32_t stage_ok = 0;    // bits 2 s, 2 s + 1: stage s holds its groups
     auto unit_of = [](const Walk& k, int j) {
-        return j < k.r.sink_units ? j : k.r.first_unit + (j - k.r.sink_units);
+        const int t = j - ATTN_ROW_COST;
+        return t < k.r.sink_units ? t : k.r.first_unit + (t - k.r.sink_units);
     };
     auto settle = [&]() {  // on to the next piece with a unit for this warp
         if (!lw.live || lj < lw.jb) return;
         Walk t = lw;
         while (t.live && lj >= t.jb) {
             walk_next(p, pre, NC, us, t);
-            lj = t.ja + w;
+            lj = own(t) + w;
         }
         __syncwarp();
         if (lane == 0) lw = t;
@@ -520,16 +552,14 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
         const int head = cw.head, col0 = (cw.row - head * cw.r.tiles) * NC, cols = cw.r.nq * p.group;
         const int tile_cols = min(NC, cols - col0);
         // ---- q: rotate, split into two FP16 parts, relative to the column's largest power of two
-        for (int c = w; c < NC; c += W) {
-            float y[4] = {};
-            if (c < tile_cols) {
-                const int j = (col0 + c) / p.group, hh = (col0 + c) - j * p.group;
-                const T* x = static_cast<const T*>(p.q) + (int64_t)(cw.r.q0 + j) * p.q_ts + (int64_t)(head * p.group + hh) * p.q_hs;
-                const uint2 u = *reinterpret_cast<const uint2*>(x + 4 * lane);
-                const T* h = reinterpret_cast<const T*>(&u);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = to_f32(h[e]);
-            }
+        for (int x = 0; x < CPW; ++x) {
+            const int c = w + x * W;
+            if (c >= NC) break;
+            float y[4];
+            const T* h = reinterpret_cast<const T*>(&qraw[x]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = to_f32(h[e]);
             if (p.rotate) rotate_warp(y, lane);
             float a = max3(fmaxf(fabsf(y[0]), fabsf(y[1])), fabsf(y[2]), fabsf(y[3]));
 #pragma unroll
@@ -554,6 +584,11 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
             }
         }
         __syncthreads();
+        if (tid == 32 * (W - 1)) {  // the next piece (read after the loop; the last warp has the fewest units)
+            Walk t = cw;
+            walk_next(p, pre, NC, us, t);
+            sh.nw = t;
+        }
         AttnState<NT> a;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -572,7 +607,7 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
         const int pos_min = sh.pos[0], pos_max = sh.pos[NC - 1];
         a.vmax = a.vinv = 0.0f;
 
-        for (int j = cw.ja + w; j < cw.jb; j += W) {
+        for (int j = own(cw) + w; j < cw.jb; j += W) {
             const int cur = st;
             st = st + 1 == S ? 0 : st + 1;
             const uint32_t ok = stage_ok >> (2 * cur) & 3u;
@@ -642,6 +677,7 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                 }
             }
         __syncthreads();
+        if (sh.nw.live) load_q(sh.nw);
         float M[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -730,7 +766,7 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
         }
         if (!complete) {
             // the CTA that arrives last joins the row's partial results, in the order of its CTAs
-            const uint32_t first = cta_of(sc, u0), last = cta_of(sc, u0 + cw.r.n - 1);
+            const uint32_t first = cta_of(sc, u0 + ATTN_ROW_COST), last = cta_of(sc, u0 + cw.r.n - 1);
             __threadfence();
             __syncthreads();
             if (tid == 0) {
@@ -760,11 +796,7 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
             }
         }
         __syncthreads();  // the merge buffer, q and the piece's record are free again
-        if (tid == 0) {
-            Walk t = cw;
-            walk_next(p, pre, NC, us, t);
-            cw = t;
-        }
+        if (tid == 0) cw = sh.nw;
         __syncthreads();
     }
 }
@@ -774,29 +806,25 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
 // used), [64 ..] arrivals per CTA, then two partial results per CTA.
 size_t attn_workspace_bytes() { return 4 * (64 + (size_t)ATTN_MAX_CTAS + 2 * (size_t)ATTN_MAX_CTAS * ATTN_PART); }
 
-#ifndef HQ_ATTN_W1
-#define HQ_ATTN_W1 8
-#define HQ_ATTN_B1 2
-#define HQ_ATTN_W2 4
-#define HQ_ATTN_B2 2
-#endif
 template <int DT, int NT, int W, int MINB> static int launch_t(const AttnParams& p, int sms, cudaStream_t st) {
     auto kernel = kv4_attention_kernel<DT, NT, W, MINB>;
-    const size_t smem = sizeof(AttnShared<NT, W>) + 8 * ((size_t)p.B + 1);
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)(sizeof(AttnShared<NT, W>) + 8 * (HQ_KV_MAX_REQUESTS + 1)));
-    if (e != cudaSuccess) return (int)e;
-    int grid = sms * MINB;
-    if (grid > ATTN_MAX_CTAS) grid = ATTN_MAX_CTAS;
-    kernel<<<grid, 32 * W, smem, st>>>(p);
+    constexpr size_t base = sizeof(AttnShared<NT, W>);
+    const int e = allow_shared(kernel, base + 8 * (HQ_KV_MAX_REQUESTS + 1));
+    if (e != (int)cudaSuccess) return e;
+    const int grid = sms * MINB < ATTN_MAX_CTAS ? sms * MINB : ATTN_MAX_CTAS;
+    kernel<<<grid, 32 * W, base + 8 * ((size_t)p.B + 1), st>>>(p);
     return (int)cudaPeekAtLastError();
 }
 
 int launch_attn(int dtype, const AttnParams& p, int sms, cudaStream_t st) {
-    const bool wide = (int64_t)p.q_len * p.group > 8;
+    // Two column tiles of 8 in one pass cost about 1.8 times one (measured at
+    // 16 requests of 8000 to 16000 tokens: 16 columns 66 us against 72 in two
+    // passes, 12 columns 64 against 71; 20 columns, three tiles, 45 against 38),
+    // so they are paired when their number is even.
+    const bool wide = ((int64_t)p.q_len * p.group + 7) / 8 % 2 == 0;
     if (dtype == HQ_DT_BF16)
-        return wide ? launch_t<HQ_DT_BF16, 2, HQ_ATTN_W2, HQ_ATTN_B2>(p, sms, st) : launch_t<HQ_DT_BF16, 1, HQ_ATTN_W1, HQ_ATTN_B1>(p, sms, st);
-    return wide ? launch_t<HQ_DT_F16, 2, HQ_ATTN_W2, HQ_ATTN_B2>(p, sms, st) : launch_t<HQ_DT_F16, 1, HQ_ATTN_W1, HQ_ATTN_B1>(p, sms, st);
+        return wide ? launch_t<HQ_DT_BF16, 2, 4, 2>(p, sms, st) : launch_t<HQ_DT_BF16, 1, 8, 2>(p, sms, st);
+    return wide ? launch_t<HQ_DT_F16, 2, 4, 2>(p, sms, st) : launch_t<HQ_DT_F16, 1, 8, 2>(p, sms, st);
 }
 
 }  // namespace hq

@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "hq_device.cuh"
 #include "hq_layer.h"
 
@@ -115,6 +117,28 @@ __device__ __forceinline__ uint2 fp8_codes8(const float (&y)[8], float s) {
         for (int i = 0; i < 4; ++i) c[i] = e4m3x2(__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s));
     }
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device;
+// asked once per kernel and device.  Returns a cudaError_t.
+template <typename K> int allow_shared(K* kernel, size_t bytes) {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<const void*> done[kMaxDevices][4];  // (kernels of one signature share this table)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return (int)e;
+    const void* const key = reinterpret_cast<const void*>(kernel);
+    if (dev >= 0 && dev < kMaxDevices)
+        for (auto& d : done[dev])
+            if (d.load(std::memory_order_acquire) == key) return (int)cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return (int)e;
+    if (dev >= 0 && dev < kMaxDevices)
+        for (auto& d : done[dev]) {
+            const void* none = nullptr;
+            if (d.compare_exchange_strong(none, key) || none == key) break;
+        }
+    return (int)cudaSuccess;
 }
 
 }  // namespace hq
