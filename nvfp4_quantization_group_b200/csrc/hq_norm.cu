@@ -27,8 +27,8 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 // A row is held by a warp (WARP) or a block of at most T threads, J chunks of
 // 8 columns a thread, chunk j of thread i being i + j * threads: a half-warp
 // holds one group of 128 columns.
-template <int DT, int WDT, int J, int T, bool WARP, bool AHEAD>
-__global__ void __launch_bounds__(T) add_rmsnorm_fp8_kernel(NormParams p) {
+template <int DT, int WDT, int J, int T, int MINB, bool WARP, bool AHEAD>
+__global__ void __launch_bounds__(T, MINB) add_rmsnorm_fp8_kernel(NormParams p) {
     __shared__ float red[2][32];
     const int lane = threadIdx.x & 31, nt = WARP ? 32 : (int)blockDim.x, i = WARP ? lane : (int)threadIdx.x;
     const int chunks = (int)(p.K / 8);
@@ -107,9 +107,9 @@ __global__ void __launch_bounds__(T) add_rmsnorm_fp8_kernel(NormParams p) {
     }
 }
 
-template <int DT, int WDT, int J, int T, bool WARP, bool AHEAD>
+template <int DT, int WDT, int J, int T, int MINB, bool WARP, bool AHEAD>
 static void norm_launch(const NormParams& p, int threads, int sms, cudaStream_t st) {
-    auto kernel = add_rmsnorm_fp8_kernel<DT, WDT, J, T, WARP, AHEAD>;
+    auto kernel = add_rmsnorm_fp8_kernel<DT, WDT, J, T, MINB, WARP, AHEAD>;
     static std::atomic<int> per_sm{0};  // resident blocks of T threads (the same on every sm_100a GPU)
     if (!per_sm) {
         int n = 0;
@@ -120,20 +120,25 @@ static void norm_launch(const NormParams& p, int threads, int sms, cudaStream_t 
     kernel<<<(unsigned)(blocks < cap ? blocks : cap), threads, 0, st>>>(p);
 }
 
-// Who holds a row (measured on BF16 rows with a residual):
+// Who holds a row.  Few rows: one chunk a thread, for the shortest chain.  Many:
+// two chunks a thread with two blocks of 512 threads an SM, so that 57 KB of the
+// next rows are in flight on each while one is worked on ([16384, 7168] BF16 with
+// a residual: 147 us, 5.6 TB/s; four chunks in blocks of 256 179 us, without the
+// loads ahead 196 us, one chunk in blocks of 1024 204 us).
 template <int DT, int WDT> static void norm_t(const NormParams& p, int sms, cudaStream_t st) {
+    constexpr int TWO = DT == HQ_DT_F32 || WDT == HQ_DT_F32 ? 1 : 2;  // (FP32 chunks need the registers of both)
     const int chunks = (int)(p.K / 8);
     auto block = [&](int j) { return ((chunks + j - 1) / j + 31) / 32 * 32; };
     if (chunks <= 128 && p.M > sms)
-        norm_launch<DT, WDT, 4, 256, true, true>(p, 256, sms, st);
+        norm_launch<DT, WDT, 4, 256, 1, true, true>(p, 256, sms, st);
     else if (chunks <= 1024 && p.M <= 2 * sms)
-        norm_launch<DT, WDT, 1, 1024, false, false>(p, block(1), sms, st);
+        norm_launch<DT, WDT, 1, 1024, 1, false, false>(p, block(1), sms, st);
     else if (chunks <= 1024)
-        norm_launch<DT, WDT, 4, 256, false, true>(p, block(4), sms, st);
+        norm_launch<DT, WDT, 2, 512, TWO, false, true>(p, block(2), sms, st);
     else if (chunks <= 4096)
-        norm_launch<DT, WDT, 8, 512, false, false>(p, block(8), sms, st);
+        norm_launch<DT, WDT, 8, 512, 1, false, false>(p, block(8), sms, st);
     else
-        norm_launch<DT, WDT, 8, 1024, false, false>(p, block(8), sms, st);
+        norm_launch<DT, WDT, 8, 1024, 1, false, false>(p, block(8), sms, st);
 }
 void launch_norm(int dtype, int w_dtype, const NormParams& p, int sms, cudaStream_t st) {
     const bool wf = w_dtype == HQ_DT_F32;
@@ -151,8 +156,8 @@ size_t norm_back_partial_floats(int64_t M, int64_t K) {
 
 // dx, and each block's sum of dw over its rows, in row order.  Rows are held
 // as in the forward kernel; a thread keeps the sums of its own columns.
-template <int DT, int WDT, int J, int T, bool WARP>
-__global__ void __launch_bounds__(T) rmsnorm_back_kernel(NormBackParams p) {
+template <int DT, int WDT, int J, int T, int MINB, bool WARP>
+__global__ void __launch_bounds__(T, MINB) rmsnorm_back_kernel(NormBackParams p) {
     __shared__ float red[2][32];
     extern __shared__ float sums[];  // WARP: [K]
     const int lane = threadIdx.x & 31, nt = WARP ? 32 : (int)blockDim.x, i = WARP ? lane : (int)threadIdx.x;
@@ -276,9 +281,9 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_join_kernel(const float* part
     if (threadIdx.x == 0) dw[(int64_t)blockIdx.x * 32 + threadIdx.y] = b;
 }
 
-template <int DT, int WDT, int J, int T, bool WARP>
+template <int DT, int WDT, int J, int T, int MINB, bool WARP>
 static int norm_back_launch(const NormBackParams& p, int threads, int sms, cudaStream_t st) {
-    auto kernel = rmsnorm_back_kernel<DT, WDT, J, T, WARP>;
+    auto kernel = rmsnorm_back_kernel<DT, WDT, J, T, MINB, WARP>;
     static std::atomic<int> per_sm{0};
     if (!per_sm) {
         int n = 0;
@@ -292,7 +297,10 @@ static int norm_back_launch(const NormBackParams& p, int threads, int sms, cudaS
     kernel<<<grid, threads, WARP ? sizeof(float) * (size_t)p.K : 0, st>>>(p);
     return grid;
 }
+// Two chunks a thread and two blocks of 512 threads an SM ([8191, 4096] BF16 with
+// dres: 52 us, 5.2 TB/s; one block an SM 61 us, four chunks a thread 54 us, one 72 us).
 template <int DT, int WDT> static void norm_back_t(const NormBackParams& p, int sms, cudaStream_t st) {
+    constexpr int TWO = DT == HQ_DT_F32 || WDT == HQ_DT_F32 ? 1 : 2;
     const int chunks = (int)(p.K / 8);
     auto block = [&](int j) { return ((chunks + j - 1) / j + 31) / 32 * 32; };
     int parts = 0;
@@ -301,11 +309,11 @@ template <int DT, int WDT> static void norm_back_t(const NormBackParams& p, int 
         return;
     }
     if (chunks <= 64) {
-        parts = norm_back_launch<DT, WDT, 2, 256, true>(p, 256, sms, st);
+        parts = norm_back_launch<DT, WDT, 2, 256, 1, true>(p, 256, sms, st);
     } else if (chunks <= 1024) {
-        parts = norm_back_launch<DT, WDT, 2, 512, false>(p, block(2), sms, st);
+        parts = norm_back_launch<DT, WDT, 2, 512, TWO, false>(p, block(2), sms, st);
     } else if (chunks <= 2048) {
-        parts = norm_back_launch<DT, WDT, 4, 512, false>(p, block(4), sms, st);
+        parts = norm_back_launch<DT, WDT, 4, 512, 1, false>(p, block(4), sms, st);
     } else {
         // (a row's sums of dw do not fit in registers; dx, which may be dy, is
         // written after dw has been taken)
@@ -314,7 +322,7 @@ template <int DT, int WDT> static void norm_back_t(const NormBackParams& p, int 
             rmsnorm_dw_kernel<DT><<<dim3((unsigned)((p.K + 255) / 256), (unsigned)parts), 256, 0, st>>>(p);
         NormBackParams q = p;
         q.dw = nullptr;
-        norm_back_launch<DT, WDT, 8, 1024, false>(q, block(8), sms, st);
+        norm_back_launch<DT, WDT, 8, 1024, 1, false>(q, block(8), sms, st);
     }
     if (p.dw) rmsnorm_dw_join_kernel<<<(unsigned)(p.K / 32), dim3(32, 32), 0, st>>>(p.partial, p.dw, p.K, parts);
 }
