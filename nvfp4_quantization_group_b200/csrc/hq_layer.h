@@ -51,7 +51,7 @@ struct RopeTensor {
 struct RopeParams {
     RopeTensor t[2];  // q, k
     int64_t T;
-    int D, R, offset, interleaved, inverse, copy;  // copy: elements outside the rotated part are passed through
+    int D, R, offset, interleaved, inverse;
     int vec;  // rows and parts are whole, aligned chunks of 8 elements
     const int64_t* pos;
     const double* inv_freq;

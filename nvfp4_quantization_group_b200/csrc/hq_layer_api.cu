@@ -199,8 +199,13 @@ hq_status hq_rope(int dtype, const void* q, int64_t q_token_stride, int64_t q_he
     p.offset = offset;
     p.interleaved = layout == HQ_ROPE_INTERLEAVED;
     p.inverse = inverse != 0;
-    p.copy = (Hq && q != q_out) || (Hk && k != k_out);
-    p.vec = 0;
+    // whole, aligned chunks of 8 elements everywhere, and a token's units within 31 bits
+    p.vec = offset % 8 == 0 && D % 8 == 0 && rotary_dim % (p.interleaved ? 8 : 16) == 0 &&
+            (int64_t)(Hq > Hk ? Hq : Hk) * (D / 8) * 4 < ((int64_t)1 << 30);
+    for (const RopeTensor& x : p.t)
+        if (x.heads)
+            p.vec = p.vec && aligned(x.in, 16) && aligned(x.out, 16) && x.in_ts % 8 == 0 && x.in_hs % 8 == 0 &&
+                    x.out_ts % 8 == 0 && x.out_hs % 8 == 0;
     p.pos = positions;
     p.inv_freq = inv_freq;
     p.magnitude = magnitude;
