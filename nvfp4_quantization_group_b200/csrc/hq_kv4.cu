@@ -177,26 +177,35 @@ void launch_slots(const SlotParams& p, int sms, cudaStream_t st) {
 constexpr int KV_THREADS = 128;
 
 struct KvShared {
-    // a vector's 32 chunks of four elements, chunk k of thread j (elements 32 j + 4 k ..) at 8 j + ((k + 2 j) & 7);
-    // 33 per vector: two vectors of a quarter-warp hit different banks on both sides
-    float4 t[32][33];
+    // a vector's 32 chunks of four elements, chunk k of thread j (elements 32 j + 4 k ..) at 8 j + ((k + j) & 7); 36
+    // per vector: the eight lanes of a quarter-warp (two vectors) hit different banks on both sides
+    float4 t[32][36];
 };
 __device__ __forceinline__ int kv_chunk(int c) {  // place of chunk c (elements 4 c .. 4 c + 3)
     const int j = c >> 3, k = c & 7;
-    return 8 * j + ((k + 2 * j) & 7);
+    return 8 * j + ((k + j) & 7);
 }
 
-// Stages h = 1, 2, .. of a butterfly over N values held by one thread.
-template <int N> __device__ __forceinline__ void butterfly(float (&y)[32], int first, int last) {
+// Stages h = first, 2 first, .. last of a butterfly over 32 values held as pairs
+// (value 2 k, 2 k + 1 in y[k]).
+__device__ __forceinline__ void butterfly(f2 (&y)[16], int first, int last) {
+    if (first <= 1) {
 #pragma unroll
-    for (int h = 1; h < N; h <<= 1) {
+        for (int k = 0; k < 16; ++k) {
+            float a, b;
+            unpack2(y[k], a, b);
+            y[k] = pack2(__fadd_rn(a, b), __fsub_rn(a, b));
+        }
+    }
+#pragma unroll
+    for (int h = 2; h < 32; h <<= 1) {
         if (h < first || h > last) continue;
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-            if ((e & h) == 0) {
-                const float a = y[e], b = y[e + h];
-                y[e] = __fadd_rn(a, b);
-                y[e + h] = __fsub_rn(a, b);
+        for (int k = 0; k < 16; ++k)
+            if ((2 * k & h) == 0) {
+                const f2 a = y[k], b = y[k + h / 2];
+                y[k] = add2(a, b);
+                y[k + h / 2] = sub2(a, b);
             }
     }
 }
@@ -209,7 +218,7 @@ __device__ __forceinline__ uint8_t* kv_group(const KvParams& p, int64_t s, int h
 }
 
 // Quantizes as hq_cat_rotate_nvfp4, bit for bit: stages in ascending order, the
-// same scales and conversions.
+// same scales and conversions.  blockIdx.y is the head.
 template <int DT> __global__ void __launch_bounds__(KV_THREADS) kv4_append_kernel(KvParams p) {
     __shared__ KvShared sh;
     __shared__ float2 vr[128];  // per E4M3 code {value, -RN(1 / value)}
@@ -220,74 +229,106 @@ template <int DT> __global__ void __launch_bounds__(KV_THREADS) kv4_append_kerne
         vr[tid] = make_float2(v, zc ? -0.0f : -__frcp_rn(v));
     }
     __syncthreads();
-    const int vec = tid >> 2, i = tid & 3, z = vec >> 4;
+    const int vec = tid >> 2, i = tid & 3, z = vec >> 4, h = blockIdx.y;
     float4* const row = sh.t[vec];
-    const int64_t tiles = (p.N + 15) / 16 * p.H;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int h = (int)(tile % p.H);
-        const int64_t tok = tile / p.H * 16 + (vec & 15);
-        const int64_t s = tok < p.N ? p.slots[tok] : -1;
-        const bool ok = s >= 0 && s < p.n_slots;  // (the four threads of a vector agree)
-        float y[32];
-        if (ok) {
-            const void* const x = z ? p.v : p.k;
-            const int64_t at = z ? tok * p.v_ts + h * p.v_hs : tok * p.k_ts + h * p.k_hs;
+    const void* const x = z ? p.v : p.k;
+    const int64_t ts = z ? p.v_ts : p.k_ts, first = (z ? p.v_hs : p.k_hs) * h + 32 * i;
+    // the vector of the next tile is on its way while one is worked on (loaded whether its slot is in use or not)
+    int64_t tok = (int64_t)blockIdx.x * 16 + (vec & 15), s = -1;
+    Chunk<DT> u[2][2] = {};
+    auto load = [&] {
+        s = -1;
+        if (tok >= p.N) return;
+        s = p.slots[tok];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) load_pair<DT>(x, tok * ts + first + 16 * c, p.wide, u[c]);
+    };
+    load();
+    while (tok - (vec & 15) < p.N) {
+        const int64_t slot = s;
+        const bool ok = slot >= 0 && slot < p.n_slots;  // (the four threads of a vector agree)
+        f2 y[16];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
                 float f[8];
-                unpack8<DT>(load_chunk<DT>(x, at + 32 * i + 8 * c), f);
+                unpack8<DT>(u[c][k], f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[8 * c + e] = f[e];
+                for (int e = 0; e < 4; ++e) y[8 * c + 4 * k + e] = pack2(f[2 * e], f[2 * e + 1]);
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = 0.0f;
         }
-        if (p.rotate) butterfly<32>(y, 1, 16);
+        tok += (int64_t)gridDim.x * 16;
+        load();
+        if (p.rotate) butterfly(y, 1, 16);
         __syncwarp();  // the last tile's reads are done
 #pragma unroll
-        for (int k = 0; k < 8; ++k) row[kv_chunk(8 * i + k)] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+        for (int k = 0; k < 8; ++k) {
+            float4 v;
+            unpack2(y[2 * k], v.x, v.y);
+            unpack2(y[2 * k + 1], v.z, v.w);
+            row[kv_chunk(8 * i + k)] = v;
+        }
         __syncwarp();
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {  // y[4 b + e]: element 16 b + 4 i + e
+        for (int b = 0; b < 8; ++b) {  // y[2 b], y[2 b + 1]: elements 16 b + 4 i .. + 3
             const float4 v = row[kv_chunk(4 * b + i)];
-            y[4 * b] = v.x;
-            y[4 * b + 1] = v.y;
-            y[4 * b + 2] = v.z;
-            y[4 * b + 3] = v.w;
+            y[2 * b] = pack2(v.x, v.y);
+            y[2 * b + 1] = pack2(v.z, v.w);
         }
         if (p.rotate) {
-            butterfly<32>(y, 8, 16);  // elements 32 and 64 apart: two and four blocks
+            butterfly(y, 8, 16);  // elements 32 and 64 apart: two and four blocks
+            const f2 c = pack2(__uint_as_float(0x3DB504F3u), __uint_as_float(0x3DB504F3u));  // RN(1 / sqrt(128))
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = __fmul_rn(y[e], __uint_as_float(0x3DB504F3u));  // RN(1 / sqrt(128))
+            for (int k = 0; k < 16; ++k) y[k] = mul2(y[k], c);
         }
-        float ab[8], amax = 0.0f;
+        float ab[8];
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
-            float a = max3(fmaxf(fabsf(y[4 * b]), fabsf(y[4 * b + 1])), fabsf(y[4 * b + 2]), fabsf(y[4 * b + 3]));
-            a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
-            ab[b] = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
-            amax = fmaxf(amax, ab[b]);
+            float a0, a1, a2, a3;
+            unpack2(y[2 * b], a0, a1);
+            unpack2(y[2 * b + 1], a2, a3);
+            ab[b] = absmax3(fmaxf(fabsf(a0), fabsf(a1)), a2, a3);
         }
+        // the four threads' maxima of each block, thread i ending with blocks 2 i and 2 i + 1
+        float m4[4], m2[2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float mine = i & 2 ? ab[4 + k] : ab[k], other = i & 2 ? ab[k] : ab[4 + k];
+            m4[k] = fmaxf(mine, __shfl_xor_sync(0xFFFFFFFFu, other, 2));
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float mine = i & 1 ? m4[2 + k] : m4[k], other = i & 1 ? m4[k] : m4[2 + k];
+            m2[k] = fmaxf(mine, __shfl_xor_sync(0xFFFFFFFFu, other, 1));
+        }
+        float amax = fmaxf(m2[0], m2[1]);
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
         const float S = global_encode(amax);
         const bool slow = slow_scale(S);
-        uint32_t codes[8], sf[2] = {0u, 0u};  // four nibbles of each block; the blocks' scales
+        const uint32_t sf0 = block_sf(m2[0], S), sf1 = block_sf(m2[1], S);
+        const float enc[2] = {block_enc(vr, sf0, S, slow), block_enc(vr, sf1, S, slow)};
+        uint32_t codes[4];
 #pragma unroll
         for (int b = 0; b < 8; b += 2) {
-            const uint32_t f0 = block_sf(ab[b], S), f1 = block_sf(ab[b + 1], S);
-            const float e0 = block_enc(vr, f0, S, slow), e1 = block_enc(vr, f1, S, slow);
-            const uint32_t c = e2m1x8(__fmul_rn(y[4 * b], e0), __fmul_rn(y[4 * b + 1], e0), __fmul_rn(y[4 * b + 2], e0),
-                                      __fmul_rn(y[4 * b + 3], e0), __fmul_rn(y[4 * b + 4], e1), __fmul_rn(y[4 * b + 5], e1),
-                                      __fmul_rn(y[4 * b + 6], e1), __fmul_rn(y[4 * b + 7], e1));
-            codes[b / 2] = c;  // bytes: block b pairs 0, 1; block b + 1 pairs 0, 1
-            sf[b / 4] |= (f0 | f1 << 8) << (8 * (b & 3));
+            float q[8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float f = __shfl_sync(0xFFFFFFFFu, enc[k], b / 2, 4);
+                const f2 f22 = pack2(f, f);
+                unpack2(mul2(y[2 * (b + k)], f22), q[4 * k], q[4 * k + 1]);
+                unpack2(mul2(y[2 * (b + k) + 1], f22), q[4 * k + 2], q[4 * k + 3]);
+            }
+            // bytes: block b pairs 0, 1; block b + 1 pairs 0, 1
+            codes[b / 2] = e2m1x8(q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7]);
         }
         if (!ok) continue;
-        uint8_t* const g = kv_group(p, s, h);
-        const int r = (int)(s & 15), half = r >> 3, pair = (r & 7) >> 1, odd = r & 1;
+        uint8_t* const g = kv_group(p, slot, h);
+        const int r = (int)(slot & 15), half = r >> 3, pair = (r & 7) >> 1, odd = r & 1;
         if (z == 0) {
             *reinterpret_cast<uint4*>(g + KV_K_CODES + r * 64 + i * 16) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
-            if (i == 0) *reinterpret_cast<uint2*>(g + KV_K_SF + r * 8) = make_uint2(sf[0], sf[1]);
+            *reinterpret_cast<uint16_t*>(g + KV_K_SF + r * 8 + 2 * i) = (uint16_t)(sf0 | sf1 << 8);
             if (i == 1) reinterpret_cast<float*>(g + KV_K_DEC)[r] = __fdiv_rn(1.0f, S);
         } else {
             // byte pairs 2 i and 2 i + 1 of the eight blocks
@@ -295,9 +336,8 @@ template <int DT> __global__ void __launch_bounds__(KV_THREADS) kv4_append_kerne
             *reinterpret_cast<uint2*>(o) = make_uint2(__byte_perm(codes[0], codes[1], 0x6420), __byte_perm(codes[2], codes[3], 0x6420));
             *reinterpret_cast<uint2*>(o + 64) = make_uint2(__byte_perm(codes[0], codes[1], 0x7531), __byte_perm(codes[2], codes[3], 0x7531));
             uint8_t* const f = g + KV_V_SF + half * 64 + pair * 16 + odd + 4 * i;  // blocks 2 i, 2 i + 1
-            const uint32_t two = (i & 2 ? sf[1] : sf[0]) >> (16 * (i & 1));
-            f[0] = (uint8_t)two;
-            f[2] = (uint8_t)(two >> 8);
+            f[0] = (uint8_t)sf0;
+            f[2] = (uint8_t)sf1;
             if (i == 1) reinterpret_cast<float*>(g + KV_V_DEC)[r] = __fdiv_rn(1.0f, S);
         }
     }
@@ -317,97 +357,117 @@ __device__ __forceinline__ void e2m1x4_to_f32(uint32_t c, float& a, float& b, fl
 
 template <int DT> __global__ void __launch_bounds__(KV_THREADS) kv4_gather_kernel(KvParams p) {
     __shared__ KvShared sh;
-    const int tid = threadIdx.x, vec = tid >> 2, i = tid & 3, z = vec >> 4;
+    const int tid = threadIdx.x, vec = tid >> 2, i = tid & 3, z = vec >> 4, h = blockIdx.y;
     float4* const row = sh.t[vec];
-    const int64_t tiles = (p.N + 15) / 16 * p.H;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int h = (int)(tile % p.H);
-        const int64_t tok = tile / p.H * 16 + (vec & 15);
-        const int64_t s = tok < p.N ? p.slots[tok] : -1;
-        float y[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] = 0.0f;
+    void* const x = z ? p.v : p.k;
+    const int64_t ts = z ? p.v_ts : p.k_ts, first = (z ? p.v_hs : p.k_hs) * h + 32 * i;
+    // a tile's codes and scales are on their way while the one before is worked on, and the slot of the one after
+    const int64_t step = (int64_t)gridDim.x * 16;
+    int64_t tok = (int64_t)blockIdx.x * 16 + (vec & 15), s = tok < p.N ? p.slots[tok] : -1;
+    uint4 codes, sf;  // keys: 16 bytes, 8 bytes; values: twice 8 bytes, 16 bytes with both tokens of the pair
+    float dec;
+    int odd;
+    auto load = [&] {  // of slot s, then the next slot
+        codes = sf = make_uint4(0u, 0u, 0u, 0u);
+        dec = 0.0f;
+        odd = (int)(s & 1);
         if (s >= 0 && s < p.n_slots) {
             const uint8_t* const g = kv_group(p, s, h);
-            const int r = (int)(s & 15), half = r >> 3, pair = (r & 7) >> 1, odd = r & 1;
-            uint32_t codes[4], sf[2];  // as in the append kernel
-            float dec;
+            const int r = (int)(s & 15), half = r >> 3, pair = (r & 7) >> 1;
             if (z == 0) {
-                const uint4 c = *reinterpret_cast<const uint4*>(g + KV_K_CODES + r * 64 + i * 16);
-                codes[0] = c.x;
-                codes[1] = c.y;
-                codes[2] = c.z;
-                codes[3] = c.w;
+                codes = *reinterpret_cast<const uint4*>(g + KV_K_CODES + r * 64 + i * 16);
                 const uint2 f = *reinterpret_cast<const uint2*>(g + KV_K_SF + r * 8);
-                sf[0] = f.x;
-                sf[1] = f.y;
-                dec = reinterpret_cast<const float*>(g + KV_K_DEC)[r];
+                sf.x = f.x;
+                sf.y = f.y;
             } else {
                 const uint8_t* const o = g + KV_V_CODES + half * 512 + 2 * i * 64 + pair * 16 + odd * 8;
                 const uint2 lo = *reinterpret_cast<const uint2*>(o), hi = *reinterpret_cast<const uint2*>(o + 64);
-                codes[0] = __byte_perm(lo.x, hi.x, 0x5140);
-                codes[1] = __byte_perm(lo.x, hi.x, 0x7362);
-                codes[2] = __byte_perm(lo.y, hi.y, 0x5140);
-                codes[3] = __byte_perm(lo.y, hi.y, 0x7362);
-                const uint4 f = *reinterpret_cast<const uint4*>(g + KV_V_SF + half * 64 + pair * 16);
-                const uint32_t pick = odd ? 0x7531 : 0x6420;
-                sf[0] = __byte_perm(f.x, f.y, pick);
-                sf[1] = __byte_perm(f.z, f.w, pick);
-                dec = reinterpret_cast<const float*>(g + KV_V_DEC)[r];
+                codes = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                sf = *reinterpret_cast<const uint4*>(g + KV_V_SF + half * 64 + pair * 16);
             }
+            dec = reinterpret_cast<const float*>(g + (z ? KV_V_DEC : KV_K_DEC))[r];
+        }
+        s = tok + step < p.N ? p.slots[tok + step] : -1;
+    };
+    load();
+    while (tok - (vec & 15) < p.N) {
+        f2 y[16];
+        {
+            uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w}, f8[2] = {sf.x, sf.y};  // in the append kernel's order
+            if (z) {
+                c[0] = __byte_perm(codes.x, codes.z, 0x5140);
+                c[1] = __byte_perm(codes.x, codes.z, 0x7362);
+                c[2] = __byte_perm(codes.y, codes.w, 0x5140);
+                c[3] = __byte_perm(codes.y, codes.w, 0x7362);
+                const uint32_t pick = odd ? 0x7531 : 0x6420;
+                f8[0] = __byte_perm(sf.x, sf.y, pick);
+                f8[1] = __byte_perm(sf.z, sf.w, pick);
+            }
+            const f2 d2 = pack2(dec, dec);
 #pragma unroll
             for (int b = 0; b < 8; ++b) {
-                float* const v = y + 4 * b;
-                e2m1x4_to_f32(codes[b / 2] >> (16 * (b & 1)), v[0], v[1], v[2], v[3]);
-                const float f = e4m3_value((sf[b / 4] >> (8 * (b & 3))) & 0xFFu);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = __fmul_rn(__fmul_rn(v[e], f), dec);
+                float v[4];
+                e2m1x4_to_f32(c[b / 2] >> (16 * (b & 1)), v[0], v[1], v[2], v[3]);
+                const float f = e4m3_value((f8[b / 4] >> (8 * (b & 3))) & 0xFFu);
+                const f2 f22 = pack2(f, f);
+                y[2 * b] = mul2(mul2(pack2(v[0], v[1]), f22), d2);
+                y[2 * b + 1] = mul2(mul2(pack2(v[2], v[3]), f22), d2);
             }
         }
+        const int64_t here = tok;
+        tok += step;
+        load();
         // stages 1, 2 and, between blocks, 16, 32, 64 here; 4 and 8 after the exchange
-        if (p.rotate) butterfly<32>(y, 1, 16);
+        if (p.rotate) butterfly(y, 1, 16);
         __syncwarp();
 #pragma unroll
-        for (int b = 0; b < 8; ++b) row[kv_chunk(4 * b + i)] = make_float4(y[4 * b], y[4 * b + 1], y[4 * b + 2], y[4 * b + 3]);
+        for (int b = 0; b < 8; ++b) {
+            float4 v;
+            unpack2(y[2 * b], v.x, v.y);
+            unpack2(y[2 * b + 1], v.z, v.w);
+            row[kv_chunk(4 * b + i)] = v;
+        }
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const float4 v = row[kv_chunk(8 * i + k)];
-            y[4 * k] = v.x;
-            y[4 * k + 1] = v.y;
-            y[4 * k + 2] = v.z;
-            y[4 * k + 3] = v.w;
+            y[2 * k] = pack2(v.x, v.y);
+            y[2 * k + 1] = pack2(v.z, v.w);
         }
         if (p.rotate) {
-            butterfly<32>(y, 4, 8);
+            butterfly(y, 4, 8);
+            const f2 c = pack2(__uint_as_float(0x3DB504F3u), __uint_as_float(0x3DB504F3u));
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = __fmul_rn(y[e], __uint_as_float(0x3DB504F3u));
+            for (int k = 0; k < 16; ++k) y[k] = mul2(y[k], c);
         }
-        if (tok >= p.N) continue;
-        void* const x = z ? p.v : p.k;
-        const int64_t at = z ? tok * p.v_ts + h * p.v_hs : tok * p.k_ts + h * p.k_hs;
+        if (here >= p.N) continue;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            float f[8];
+        for (int c = 0; c < 2; ++c) {
+            Chunk<DT> u[2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = y[8 * c + e];
-            store_chunk<DT>(x, at + 32 * i + 8 * c, pack8<DT>(f));
+            for (int k = 0; k < 2; ++k) {
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) unpack2(y[8 * c + 4 * k + e], f[2 * e], f[2 * e + 1]);
+                u[k] = pack8<DT>(f);
+            }
+            store_pair<DT>(x, here * ts + first + 16 * c, p.wide, u);
         }
     }
 }
 
-static int kv_grid(const KvParams& p, int sms) {
-    const int64_t tiles = (p.N + 15) / 16 * p.H, cap = (int64_t)sms * 8;
-    return (int)(tiles < cap ? tiles : cap);
+static dim3 kv_grid(const KvParams& p, int sms) {
+    const int64_t tiles = (p.N + 15) / 16, cap = ((int64_t)sms * 8 + p.H - 1) / p.H;
+    return dim3((unsigned)(tiles < cap ? tiles : cap), (unsigned)p.H);
 }
 void launch_append(int dtype, const KvParams& p, int sms, cudaStream_t st) {
-    const int grid = kv_grid(p, sms);
+    const dim3 grid = kv_grid(p, sms);
     if (dtype == HQ_DT_BF16) kv4_append_kernel<HQ_DT_BF16><<<grid, KV_THREADS, 0, st>>>(p);
     else if (dtype == HQ_DT_F16) kv4_append_kernel<HQ_DT_F16><<<grid, KV_THREADS, 0, st>>>(p);
     else kv4_append_kernel<HQ_DT_F32><<<grid, KV_THREADS, 0, st>>>(p);
 }
 void launch_gather(int dtype, const KvParams& p, int sms, cudaStream_t st) {
-    const int grid = kv_grid(p, sms);
+    const dim3 grid = kv_grid(p, sms);
     if (dtype == HQ_DT_BF16) kv4_gather_kernel<HQ_DT_BF16><<<grid, KV_THREADS, 0, st>>>(p);
     else if (dtype == HQ_DT_F16) kv4_gather_kernel<HQ_DT_F16><<<grid, KV_THREADS, 0, st>>>(p);
     else kv4_gather_kernel<HQ_DT_F32><<<grid, KV_THREADS, 0, st>>>(p);

@@ -49,6 +49,36 @@ template <int DT> __device__ __forceinline__ void store_chunk(void* base, int64_
     p[0] = c.w[0];
     if constexpr (DT == HQ_DT_F32) p[1] = c.w[1];
 }
+// Sixteen elements: where they are 32-byte aligned (the caller's word for it), as
+// 32-byte accesses, a whole sector each.
+template <int DT> __device__ __forceinline__ void load_pair(const void* base, int64_t elem, bool wide, Chunk<DT> (&c)[2]) {
+    const typename Elem<DT>::T* const p = static_cast<const typename Elem<DT>::T*>(base) + elem;
+    if (!wide) {
+        c[0] = load_chunk<DT>(base, elem);
+        c[1] = load_chunk<DT>(base, elem + 8);
+    } else if constexpr (DT == HQ_DT_F32) {
+        ld_nc_v8(p, c[0].w[0], c[0].w[1]);
+        ld_nc_v8(p + 8, c[1].w[0], c[1].w[1]);
+    } else {
+        ld_nc_v8(p, c[0].w[0], c[1].w[0]);
+    }
+}
+__device__ __forceinline__ void st_v8(void* p, const uint4& a, const uint4& b) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w) : "memory");
+}
+template <int DT> __device__ __forceinline__ void store_pair(void* base, int64_t elem, bool wide, const Chunk<DT> (&c)[2]) {
+    typename Elem<DT>::T* const p = static_cast<typename Elem<DT>::T*>(base) + elem;
+    if (!wide) {
+        store_chunk<DT>(base, elem, c[0]);
+        store_chunk<DT>(base, elem + 8, c[1]);
+    } else if constexpr (DT == HQ_DT_F32) {
+        st_v8(p, c[0].w[0], c[0].w[1]);
+        st_v8(p + 8, c[1].w[0], c[1].w[1]);
+    } else {
+        st_v8(p, c[0].w[0], c[1].w[0]);
+    }
+}
 template <int DT> __device__ __forceinline__ void unpack8(const Chunk<DT>& c, float (&f)[8]) {
     if constexpr (DT == HQ_DT_F32) {
         const uint32_t u[8] = {c.w[0].x, c.w[0].y, c.w[0].z, c.w[0].w, c.w[1].x, c.w[1].y, c.w[1].z, c.w[1].w};

@@ -90,6 +90,7 @@ struct KvParams {
     uint8_t* cache;
     int64_t n_slots;  // num_pages * page_size
     int page_shift;
+    int wide;  // k and v: 32-byte aligned vectors
 };
 void launch_append(int dtype, const KvParams& p, int sms, cudaStream_t st);
 void launch_gather(int dtype, const KvParams& p, int sms, cudaStream_t st);

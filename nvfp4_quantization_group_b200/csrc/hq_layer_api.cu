@@ -199,9 +199,8 @@ hq_status hq_rope(int dtype, const void* q, int64_t q_token_stride, int64_t q_he
     p.offset = offset;
     p.interleaved = layout == HQ_ROPE_INTERLEAVED;
     p.inverse = inverse != 0;
-    // whole, aligned chunks of 8 elements everywhere, and a token's units within 31 bits
-    p.vec = offset % 8 == 0 && D % 8 == 0 && rotary_dim % (p.interleaved ? 8 : 16) == 0 &&
-            (int64_t)(Hq > Hk ? Hq : Hk) * (D / 8) * 4 < ((int64_t)1 << 30);
+    // whole, aligned chunks of 8 elements everywhere, at most 256 to a head
+    p.vec = offset % 8 == 0 && D % 8 == 0 && D <= 2048 && rotary_dim % (p.interleaved ? 8 : 16) == 0;
     for (const RopeTensor& x : p.t)
         if (x.heads)
             p.vec = p.vec && aligned(x.in, 16) && aligned(x.out, 16) && x.in_ts % 8 == 0 && x.in_hs % 8 == 0 &&
@@ -286,6 +285,7 @@ static hq_status kv4_params(int dtype, const void* k, int64_t k_ts, int64_t k_hs
     p.cache = const_cast<uint8_t*>(cache);
     p.n_slots = num_pages << shift;
     p.page_shift = shift;
+    p.wide = aligned(k, 32) && aligned(v, 32) && k_ts % 16 == 0 && k_hs % 16 == 0 && v_ts % 16 == 0 && v_hs % 16 == 0;
     return HQ_OK;
 }
 

@@ -27,94 +27,100 @@ __device__ __forceinline__ void rope_turn(float& u, float& v, float2 r) {
     u = a;
 }
 
-// Quotient and remainder by a divisor below 2^16 with m = floor((2^32 - 1) / d).
-__device__ __forceinline__ uint32_t rope_div(uint32_t x, uint32_t d, uint32_t m, uint32_t& r) {
-    uint32_t q = __umulhi(x, m);
-    r = x - q * d;
-    while (r >= d) {
-        ++q;
-        r -= d;
-    }
-    return q;
-}
-
 // ------------------------------------------------------------- wide chunks
-// TT tokens a block (blockIdx.x), the heads' units split over blockIdx.y.  A
-// unit is 8 pairs (two chunks of 8 elements, HALVES), 4 pairs (one chunk,
-// INTERLEAVED) or a chunk passed through; a thread has UN of them in flight.
+// A unit is 8 pairs (two chunks of 8 elements, HALVES), 4 pairs (one chunk,
+// INTERLEAVED) or a chunk passed through.  A thread has the same unit of every
+// head that it takes, so blockDim.x is a multiple of the units per head; the
+// heads of q and k of TT tokens (blockIdx.x) go round over the threads' groups and
+// blockIdx.y.  UN units of a thread are in flight, the first ones while the
+// angles are formed.
 template <int DT, bool INTER, int TT>
 __global__ void __launch_bounds__(ROPE_THREADS) rope_vec_kernel(RopeParams p) {
-    constexpr int UN = DT == HQ_DT_F32 ? 2 : 4;
-    extern __shared__ float2 cs[];  // [TT][R / 2]
-    const int half = p.R / 2;
+    constexpr int UN = DT == HQ_DT_F32 ? 2 : 4, V4 = INTER ? 2 : 4;  // float4s of cosines and sines per unit
+    extern __shared__ float4 cs[];  // [TT][V4][units turned]: no bank conflicts between a warp's units
     const int64_t t0 = (int64_t)blockIdx.x * TT;
-    const int tokens = p.T - t0 < TT ? (int)(p.T - t0) : TT;
-    for (int n = threadIdx.x; n < tokens * half; n += ROPE_THREADS) {
-        const int t = n / half, i = n - t * half;
-        cs[n] = rope_cos_sin(p.pos[t0 + t], p.inv_freq[i], p.magnitude, p.inverse != 0);
+    const int tokens = p.T - t0 < TT ? (int)(p.T - t0) : TT, half = p.R / 2;
+    const int turned = half / (2 * V4), rest = (p.D - p.R) / 8;
+    const bool copy[2] = {p.t[0].in != p.t[0].out, p.t[1].heads && p.t[1].in != p.t[1].out};
+    const int per_head = turned + (copy[0] || copy[1] ? rest : 0), groups = blockDim.x / per_head;
+    const int u = threadIdx.x % per_head, heads = p.t[0].heads + p.t[1].heads;
+    const bool turn = u < turned;
+    int e = p.offset + 8 * u;  // first element
+    if (!turn) e = u - turned < p.offset / 8 ? 8 * (u - turned) : 8 * (u - turned) + p.R;
+    // the thread's next (token, head), as token * heads + head
+    int head = blockIdx.y * groups + threadIdx.x / per_head, t = 0;
+    const int step = gridDim.y * groups;
+    auto settle = [&] {
+        while (head >= heads) {
+            head -= heads;
+            ++t;
+        }
+    };
+    settle();
+    Chunk<DT> a[UN], b[UN];
+    int64_t at[UN];  // output element of the first chunk
+    int tok[UN];     // token; bit 8: k; -1: none
+    auto load = [&] {
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+            tok[k] = -1;
+            if (t >= tokens) continue;
+            const bool z = head >= p.t[0].heads;
+            const RopeTensor& x = p.t[z];
+            const int64_t h = z ? head - p.t[0].heads : head;
+            if (turn || copy[z]) {
+                const int64_t src = (t0 + t) * x.in_ts + h * x.in_hs + e;
+                at[k] = (t0 + t) * x.out_ts + h * x.out_hs + e;
+                a[k] = load_chunk<DT>(x.in, src);
+                if (!INTER && turn) b[k] = load_chunk<DT>(x.in, src + half);
+                tok[k] = t | (z ? 256 : 0);
+            }
+            head += step;
+            settle();
+        }
+    };
+    load();
+    for (int n = threadIdx.x; n < tokens * half; n += blockDim.x) {
+        const int q = n / half, i = n - q * half;
+        const float2 v = rope_cos_sin(p.pos[t0 + q], p.inv_freq[i], p.magnitude, p.inverse != 0);
+        const int at4 = (q * V4 + i % (2 * V4) / 2) * turned + i / (2 * V4);
+        reinterpret_cast<float2*>(cs)[2 * at4 + (i & 1)] = v;
     }
     __syncthreads();
-    const uint32_t turned = INTER ? p.R / 8 : p.R / 16, before = p.offset / 8;
-#pragma unroll 1
-    for (int z = 0; z < 2; ++z) {
-        const RopeTensor& x = p.t[z];
-        if (x.heads == 0) continue;
-        const uint32_t per_head = turned + (x.in != x.out ? (p.D - p.R) / 8 : 0);
-        const uint32_t per_token = per_head * x.heads, total = per_token * tokens;
-        const uint32_t head_m = 0xFFFFFFFFu / per_head, token_m = 0xFFFFFFFFu / per_token;
-        for (uint32_t n0 = blockIdx.y * ROPE_THREADS + threadIdx.x; n0 < total; n0 += gridDim.y * ROPE_THREADS * UN) {
-            Chunk<DT> a[UN], b[UN];
-            int64_t at[UN];   // output element of the first chunk
-            int unit[UN];     // unit of the head; token << 16
+    for (bool more = true; more;) {
+        more = t < tokens;
 #pragma unroll
-            for (int k = 0; k < UN; ++k) {
-                const uint32_t n = n0 + k * gridDim.y * ROPE_THREADS;
-                unit[k] = -1;
-                if (n >= total) continue;
-                uint32_t in_token, u;
-                const uint32_t t = TT == 1 ? (in_token = n, 0u) : rope_div(n, per_token, token_m, in_token);
-                const uint32_t head = rope_div(in_token, per_head, head_m, u);
-                uint32_t e;  // first element
-                if (u < turned) e = p.offset + 8 * u;
-                else e = u - turned < before ? 8 * (u - turned) : 8 * (u - turned) + p.R;
-                const int64_t src = (t0 + t) * x.in_ts + (int64_t)head * x.in_hs + e;
-                at[k] = (t0 + t) * x.out_ts + (int64_t)head * x.out_hs + e;
-                a[k] = load_chunk<DT>(x.in, src);
-                if (!INTER && u < turned) b[k] = load_chunk<DT>(x.in, src + half);
-                unit[k] = (int)(t << 16 | u);
+        for (int k = 0; k < UN; ++k) {
+            if (tok[k] < 0) continue;
+            void* const out = p.t[tok[k] >> 8].out;
+            if (!turn) {
+                store_chunk<DT>(out, at[k], a[k]);
+                continue;
             }
+            const float4* const r = cs + (tok[k] & 255) * V4 * turned + u;
+            float f[8];
+            unpack8<DT>(a[k], f);
+            if constexpr (INTER) {
 #pragma unroll
-            for (int k = 0; k < UN; ++k) {
-                if (unit[k] < 0) continue;
-                const uint32_t u = unit[k] & 0xFFFF, t = (uint32_t)unit[k] >> 16;
-                if (u < turned) {
-                    float f[8];
-                    unpack8<DT>(a[k], f);
-                    const float4* r = reinterpret_cast<const float4*>(cs + t * half + (INTER ? 4 : 8) * u);
-                    if constexpr (INTER) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float4 v = r[e];
-                            rope_turn(f[4 * e], f[4 * e + 1], make_float2(v.x, v.y));
-                            rope_turn(f[4 * e + 2], f[4 * e + 3], make_float2(v.z, v.w));
-                        }
-                    } else {
-                        float g[8];
-                        unpack8<DT>(b[k], g);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float4 v = r[e];
-                            rope_turn(f[2 * e], g[2 * e], make_float2(v.x, v.y));
-                            rope_turn(f[2 * e + 1], g[2 * e + 1], make_float2(v.z, v.w));
-                        }
-                        store_chunk<DT>(x.out, at[k] + half, pack8<DT>(g));
-                    }
-                    store_chunk<DT>(x.out, at[k], pack8<DT>(f));
-                } else {
-                    store_chunk<DT>(x.out, at[k], a[k]);
+                for (int i = 0; i < 2; ++i) {
+                    const float4 v = r[i * turned];
+                    rope_turn(f[4 * i], f[4 * i + 1], make_float2(v.x, v.y));
+                    rope_turn(f[4 * i + 2], f[4 * i + 3], make_float2(v.z, v.w));
                 }
+            } else {
+                float g[8];
+                unpack8<DT>(b[k], g);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 v = r[i * turned];
+                    rope_turn(f[2 * i], g[2 * i], make_float2(v.x, v.y));
+                    rope_turn(f[2 * i + 1], g[2 * i + 1], make_float2(v.z, v.w));
+                }
+                store_chunk<DT>(out, at[k] + half, pack8<DT>(g));
             }
+            store_chunk<DT>(out, at[k], pack8<DT>(f));
         }
+        if (more) load();
     }
 }
 
@@ -123,11 +129,11 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_vec_kernel(RopeParams p) {
 template <int DT>
 __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(RopeParams p) {
     typedef typename Elem<DT>::T T;
-    extern __shared__ float2 cs[];  // [R / 2]
+    extern __shared__ float2 angles[];  // [R / 2]
     const int64_t t = blockIdx.x;
     const int half = p.R / 2;
     for (int i = threadIdx.x; i < half; i += ROPE_THREADS)
-        cs[i] = rope_cos_sin(p.pos[t], p.inv_freq[i], p.magnitude, p.inverse != 0);
+        angles[i] = rope_cos_sin(p.pos[t], p.inv_freq[i], p.magnitude, p.inverse != 0);
     __syncthreads();
     for (int z = 0; z < 2; ++z) {
         const RopeTensor& x = p.t[z];
@@ -141,7 +147,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(RopeParams p) {
             if (i < half) {
                 const int e = p.offset + (p.interleaved ? 2 * i : i), f = e + (p.interleaved ? 1 : half);
                 float u = to_f32(a[e]), v = to_f32(a[f]);
-                rope_turn(u, v, cs[i]);
+                rope_turn(u, v, angles[i]);
                 b[e] = from_f32<DT>(u);
                 b[f] = from_f32<DT>(v);
             } else {
@@ -152,26 +158,29 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(RopeParams p) {
     }
 }
 
-template <int DT, int TT> static void rope_vec(const RopeParams& p, int split, cudaStream_t st) {
+template <int DT, int TT> static void rope_vec(const RopeParams& p, int threads, int split, cudaStream_t st) {
     const dim3 grid((unsigned)((p.T + TT - 1) / TT), (unsigned)split);
     const size_t smem = sizeof(float2) * (size_t)(p.R / 2) * TT;
-    if (p.interleaved) rope_vec_kernel<DT, true, TT><<<grid, ROPE_THREADS, smem, st>>>(p);
-    else rope_vec_kernel<DT, false, TT><<<grid, ROPE_THREADS, smem, st>>>(p);
+    if (p.interleaved) rope_vec_kernel<DT, true, TT><<<grid, threads, smem, st>>>(p);
+    else rope_vec_kernel<DT, false, TT><<<grid, threads, smem, st>>>(p);
 }
 template <int DT> static void rope_t(const RopeParams& p, int sms, cudaStream_t st) {
     if (!p.vec) {
         rope_kernel<DT><<<(unsigned)p.T, ROPE_THREADS, sizeof(float2) * (size_t)(p.R / 2), st>>>(p);
         return;
     }
-    // Many tokens: four a block, so that every thread has an angle to form.  Few:
-    // the heads of a token over several blocks, up to two per SM.
-    if (p.T >= 4 * sms && p.R <= 1024) {
-        rope_vec<DT, 4>(p, 1, st);
+    bool copy = false;
+    for (const RopeTensor& x : p.t) copy = copy || (x.heads && x.in != x.out);
+    const int per_head = p.R / (p.interleaved ? 8 : 16) + (copy ? (p.D - p.R) / 8 : 0), groups = ROPE_THREADS / per_head;
+    // Many tokens: four a block, so that a thread has an angle or more to form.
+    // Few: the heads of a token over several blocks, up to two blocks per SM.
+    if (p.T >= 4 * sms) {
+        rope_vec<DT, 4>(p, groups * per_head, 1, st);
     } else {
-        const int64_t units = ((int64_t)p.t[0].heads + p.t[1].heads) * (p.D / 8);
-        int64_t split = (2 * sms + p.T - 1) / p.T, most = (units + ROPE_THREADS - 1) / ROPE_THREADS;
+        const int64_t most = (p.t[0].heads + p.t[1].heads + groups - 1) / groups;
+        int64_t split = (2 * sms + p.T - 1) / p.T;
         if (split > most) split = most;
-        rope_vec<DT, 1>(p, (int)(split < 1 ? 1 : split), st);
+        rope_vec<DT, 1>(p, groups * per_head, (int)split, st);
     }
 }
 void launch_rope(int dtype, const RopeParams& p, int sms, cudaStream_t st) {
