@@ -60,6 +60,20 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+def _vector(what: str, name: str, t: torch.Tensor, n: int, dtype) -> None:
+    """Refuses anything but a contiguous [n] tensor of the type."""
+    if t.dtype == dtype and t.dim() == 1 and t.shape[0] == n and t.is_contiguous():
+        return
+    raise HQError(HQ_ERR_UNSUPPORTED if t.dtype != dtype else HQ_ERR_SHAPE, f"{what}: {name}'s type or shape")
+
+
+def _table(what: str, t: torch.Tensor, B: int) -> int:
+    """Width of a contiguous int32 [B, width] block table."""
+    if t.dtype == torch.int32 and t.dim() == 2 and t.shape[0] == B and t.is_contiguous():
+        return t.shape[1]
+    raise HQError(HQ_ERR_UNSUPPORTED if t.dtype != torch.int32 else HQ_ERR_SHAPE, f"{what}: block_table's type or shape")
+
+
 def _device(what: str, first: torch.Tensor, *others) -> int:
     """Index of the CUDA device that all tensors are on."""
     d = first.get_device()
@@ -110,10 +124,8 @@ def hq_rmsnorm_backward(dtype, dy, dy_row_stride, h, h_row_stride, weight, w_dty
 
 def _rows(what: str, name: str, t: torch.Tensor, shape, dtype) -> int:
     """Row stride of a tensor of the given [M, K] and type with contiguous rows."""
-    if t.shape != shape:
-        raise HQError(HQ_ERR_SHAPE, f"{what}: {name}'s shape")
-    if t.dtype != dtype:
-        raise HQError(HQ_ERR_UNSUPPORTED, f"{what}: {name}'s type")
+    if t.shape != shape or t.dtype != dtype:
+        raise HQError(HQ_ERR_SHAPE if t.dtype == dtype else HQ_ERR_UNSUPPORTED, f"{what}: {name}'s type or shape")
     row, one = t.stride()
     if one != 1:
         raise HQError(HQ_ERR_ALIGN, f"{what}: {name}'s rows are not contiguous")
@@ -121,10 +133,8 @@ def _rows(what: str, name: str, t: torch.Tensor, shape, dtype) -> int:
 
 
 def _weight(what: str, w: torch.Tensor, K: int, dtype) -> int:
-    _need(w.shape == (K,) and w.is_contiguous(), HQ_ERR_SHAPE, what, "weight's shape")
-    t = w.dtype
-    _need(t == dtype or t == torch.float32, HQ_ERR_UNSUPPORTED, what, "weight's type")
-    return _DTYPE[t]
+    _vector(what, "weight", w, K, dtype if w.dtype == dtype else torch.float32)
+    return _DTYPE[w.dtype]
 
 
 def add_rmsnorm_fp8_k128(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
@@ -135,8 +145,8 @@ def add_rmsnorm_fp8_k128(x: torch.Tensor, weight: torch.Tensor, residual: torch.
     itself) and, when asked, rstd [M] and amax."""
     what = "add_rmsnorm_fp8_k128"
     shape, dtype = x.shape, x.dtype
-    _need(len(shape) == 2, HQ_ERR_SHAPE, what, "x is [M, K]")
-    _need(dtype in _DTYPE, HQ_ERR_UNSUPPORTED, what, "x's type")
+    if len(shape) != 2 or dtype not in _DTYPE:
+        raise HQError(HQ_ERR_SHAPE if dtype in _DTYPE else HQ_ERR_UNSUPPORTED, what + ": x is [M, K]")
     dev = _device(what, x, weight, residual, residual_out)
     M, K = shape
     xs, rs = _rows(what, "x", x, shape, dtype), 0 if residual is None else _rows(what, "residual", residual, shape, dtype)
@@ -186,15 +196,14 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rs
     dx is written into `dx` where given (it may be dy or dres itself)."""
     what = "rmsnorm_backward"
     shape, dtype = dy.shape, dy.dtype
-    _need(len(shape) == 2, HQ_ERR_SHAPE, what, "dy is [M, K]")
-    _need(dtype in _DTYPE, HQ_ERR_UNSUPPORTED, what, "dy's type")
+    if len(shape) != 2 or dtype not in _DTYPE:
+        raise HQError(HQ_ERR_SHAPE if dtype in _DTYPE else HQ_ERR_UNSUPPORTED, what + ": dy is [M, K]")
     dev = _device(what, dy, h, weight, rstd, dres, ws, dx)
     M, K = shape
     gs, hs = _rows(what, "dy", dy, shape, dtype), _rows(what, "h", h, shape, dtype)
     rs = 0 if dres is None else _rows(what, "dres", dres, shape, dtype)
     wd = _weight(what, weight, K, dtype)
-    _need(rstd.shape == (M,) and rstd.is_contiguous(), HQ_ERR_SHAPE, what, "rstd's shape")
-    _need(rstd.dtype == torch.float32, HQ_ERR_UNSUPPORTED, what, "rstd's type")
+    _vector(what, "rstd", rstd, M, torch.float32)
     if dx is not None:
         _rows(what, "dx", dx, shape, dtype)
         _need(dx.is_contiguous(), HQ_ERR_ALIGN, what, "dx is not contiguous")
@@ -213,10 +222,8 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rs
 
 def _heads(what: str, name: str, t: torch.Tensor, shape, dtype):
     """Token and head strides of a [T, heads, D] tensor of the given shape and type with contiguous rows."""
-    if t.shape != shape:
-        raise HQError(HQ_ERR_SHAPE, f"{what}: {name}'s shape")
-    if t.dtype != dtype:
-        raise HQError(HQ_ERR_UNSUPPORTED, f"{what}: {name}'s type")
+    if t.shape != shape or t.dtype != dtype:
+        raise HQError(HQ_ERR_SHAPE if t.dtype == dtype else HQ_ERR_UNSUPPORTED, f"{what}: {name}'s type or shape")
     token, head, one = t.stride()
     if one != 1 and shape[2] > 1:
         raise HQError(HQ_ERR_ALIGN, f"{what}: {name}'s rows are not contiguous")
@@ -259,21 +266,22 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_f
     inverse=True is the gradient with respect to the inputs."""
     what = "rope"
     shape, dtype = q.shape, q.dtype
-    _need(len(shape) == 3, HQ_ERR_SHAPE, what, "q is [T, heads, D]")
-    _need(dtype in _DTYPE, HQ_ERR_UNSUPPORTED, what, "q's type")
+    if len(shape) != 3 or dtype not in _DTYPE:
+        raise HQError(HQ_ERR_SHAPE if dtype in _DTYPE else HQ_ERR_UNSUPPORTED, what + ": q is [T, heads, D]")
     dev = _device(what, q, k, positions, inv_freq, q_out, k_out)
     T, Hq, D = shape
     qs = _heads(what, "q", q, shape, dtype)
     kshape, ks, Hk = None, (0, 0), 0
     if k is not None:
         kshape = k.shape
-        _need(len(kshape) == 3 and kshape[0] == T and kshape[2] == D, HQ_ERR_SHAPE, what, "k's shape")
+        if len(kshape) != 3 or kshape[0] != T or kshape[2] != D:
+            raise HQError(HQ_ERR_SHAPE, what + ": k's shape")
         ks, Hk = _heads(what, "k", k, kshape, dtype), kshape[1]
-    _need(k is not None or k_out is None, HQ_ERR_SHAPE, what, "k_out without k")
-    _need(positions.shape == (T,) and positions.is_contiguous(), HQ_ERR_SHAPE, what, "positions' shape")
-    _need(positions.dtype == torch.int64, HQ_ERR_UNSUPPORTED, what, "positions' type")
-    _need(inv_freq.dim() == 1 and inv_freq.is_contiguous(), HQ_ERR_SHAPE, what, "inv_freq's shape")
-    _need(inv_freq.dtype == torch.float64, HQ_ERR_UNSUPPORTED, what, "inv_freq's type")
+    elif k_out is not None:
+        raise HQError(HQ_ERR_SHAPE, what + ": k_out without k")
+    _vector(what, "positions", positions, T, torch.int64)
+    half = inv_freq.shape[0] if inv_freq.dim() == 1 else -1
+    _vector(what, "inv_freq", inv_freq, half, torch.float64)
     qos = (Hq * D, D) if q_out is None else _heads(what, "q_out", q_out, shape, dtype)
     kos = (Hk * D, D) if k_out is None else _heads(what, "k_out", k_out, kshape, dtype)
 
@@ -281,7 +289,7 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_f
         qo = q.new_empty(shape) if q_out is None else q_out
         ko = k.new_empty(kshape) if k is not None and k_out is None else k_out
         _check(lib().hq_rope(_DTYPE[dtype], q.data_ptr(), qs[0], qs[1], Hq, _ptr(k), ks[0], ks[1], Hk, T, D,
-                             positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0], offset, layout, magnitude,
+                             positions.data_ptr(), inv_freq.data_ptr(), 2 * half, offset, layout, magnitude,
                              1 if inverse else 0, qo.data_ptr(), qos[0], qos[1], _ptr(ko), kos[0], kos[1], s), what)
         return qo, ko
 
@@ -305,27 +313,27 @@ def kv_slots(lens: torch.Tensor, new_tokens: torch.Tensor, block_table: torch.Te
     what = "kv_slots"
     dev = _device(what, lens, new_tokens, block_table, free_pages, free_count, lens_out, free_count_out)
     B = lens.shape[0] if lens.dim() == 1 else -1
-    width = block_table.shape[-1] if block_table.dim() == 2 else -1
-    for name, t, shape in (("lens", lens, (B,)), ("new_tokens", new_tokens, (B,)), ("block_table", block_table, (B, width)),
-                           ("free_pages", free_pages, (free_pages.numel(),)), ("free_count", free_count, (1,)),
-                           ("lens_out", lens_out, (B,)), ("free_count_out", free_count_out, (1,))):
-        if t is None:
-            continue
-        if t.shape != shape or not t.is_contiguous():
-            raise HQError(HQ_ERR_SHAPE, f"{what}: {name}'s shape")
-        if t.dtype != torch.int32:
-            raise HQError(HQ_ERR_UNSUPPORTED, f"{what}: {name}'s type")
+    i32 = torch.int32
+    _vector(what, "lens", lens, B, i32)
+    _vector(what, "new_tokens", new_tokens, B, i32)
+    width = _table(what, block_table, B)
+    capacity = free_pages.numel()
+    _vector(what, "free_pages", free_pages, capacity, i32)
+    _vector(what, "free_count", free_count, 1, i32)
+    if lens_out is not None:
+        _vector(what, "lens_out", lens_out, B, i32)
+    if free_count_out is not None:
+        _vector(what, "free_count_out", free_count_out, 1, i32)
     _need(n_slots >= 0, HQ_ERR_SHAPE, what, "n_slots")
 
     def call(s):
-        lo, cu, count, status = lens.new_empty((2 * B + 3,)).split((B, B + 1, 1, 1))
-        if lens_out is not None:
-            lo = lens_out
-        if free_count_out is not None:
-            count = free_count_out
-        slots, positions = lens.new_empty((2, n_slots), dtype=torch.int64).unbind()
+        lo = torch.empty_like(lens) if lens_out is None else lens_out
+        count = torch.empty_like(free_count) if free_count_out is None else free_count_out
+        cu, status = lens.new_empty((B + 1,)), torch.empty_like(free_count)
+        slots = lens.new_empty((n_slots,), dtype=torch.int64)
+        positions = torch.empty_like(slots)
         _check(lib().hq_kv_slots(B, lens.data_ptr(), new_tokens.data_ptr(), block_table.data_ptr(), width,
-                                 free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(), page_size, n_slots,
+                                 free_pages.data_ptr(), capacity, free_count.data_ptr(), page_size, n_slots,
                                  lo.data_ptr(), cu.data_ptr(), slots.data_ptr(), positions.data_ptr(), count.data_ptr(),
                                  status.data_ptr(), s), what)
         return {"lens": lo, "cu_new": cu, "slots": slots, "positions": positions, "free_count": count, "status": status}
@@ -347,9 +355,9 @@ def kv4_cache(num_pages: int, page_size: int, H: int, device="cuda") -> torch.Te
 def _cache_shape(what: str, cache: torch.Tensor):
     """(pages, page_size, heads) of a cache."""
     shape = cache.shape
-    _need(len(shape) == 4 and shape[3] == HQ_KV4_GROUP_BYTES and cache.is_contiguous(), HQ_ERR_SHAPE, what,
-          "the cache is [pages, heads, page_size / 16, 2432], contiguous")
-    _need(cache.dtype == torch.uint8, HQ_ERR_UNSUPPORTED, what, "the cache's type")
+    if len(shape) != 4 or shape[3] != HQ_KV4_GROUP_BYTES or cache.dtype != torch.uint8 or not cache.is_contiguous():
+        raise HQError(HQ_ERR_SHAPE if cache.dtype == torch.uint8 else HQ_ERR_UNSUPPORTED,
+                      what + ": the cache is uint8 [pages, heads, page_size / 16, 2432], contiguous")
     return shape[0], shape[2] * HQ_KV4_GROUP_TOKENS, shape[1]
 
 
@@ -368,9 +376,9 @@ def hq_kv4_gather(dtype, cache, num_pages, page_size, slots, N, H, hadamard_n, k
 
 
 def _slots_arg(what: str, slots: torch.Tensor) -> int:
-    _need(slots.dim() == 1 and slots.is_contiguous(), HQ_ERR_SHAPE, what, "slots' shape")
-    _need(slots.dtype == torch.int64, HQ_ERR_UNSUPPORTED, what, "slots' type")
-    return slots.shape[0]
+    n = slots.numel()
+    _vector(what, "slots", slots, n, torch.int64)
+    return n
 
 
 def kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor, hadamard_n: int = 128,
@@ -381,7 +389,8 @@ def kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: tor
     pages, page, H = _cache_shape(what, cache)
     N, dtype = _slots_arg(what, slots), k.dtype
     _need(dtype in _DTYPE, HQ_ERR_UNSUPPORTED, what, "k's type")
-    (kt, kh), (vt, vh) = (_heads(what, n, t, (N, H, HQ_KV4_HEAD), dtype) for n, t in (("k", k), ("v", v)))
+    shape = (N, H, HQ_KV4_HEAD)
+    (kt, kh), (vt, vh) = _heads(what, "k", k, shape, dtype), _heads(what, "v", v, shape, dtype)
 
     def call(s):
         _check(lib().hq_kv4_append(_DTYPE[dtype], k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(), N, H,
@@ -400,7 +409,8 @@ def kv4_gather(cache: torch.Tensor, slots: torch.Tensor, dtype: torch.dtype = to
     _need(dtype in _DTYPE, HQ_ERR_UNSUPPORTED, what, "dtype")
 
     def call(s):
-        k, v = cache.new_empty((2, N, H, HQ_KV4_HEAD), dtype=dtype).unbind()
+        k = cache.new_empty((N, H, HQ_KV4_HEAD), dtype=dtype)
+        v = torch.empty_like(k)
         t = H * HQ_KV4_HEAD
         _check(lib().hq_kv4_gather(_DTYPE[dtype], cache.data_ptr(), pages, page, slots.data_ptr(), N, H, hadamard_n,
                                    k.data_ptr(), t, HQ_KV4_HEAD, v.data_ptr(), t, HQ_KV4_HEAD, s), what)
@@ -443,20 +453,17 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     dev = _device(what, q, cache, block_table, seq_lens, cu_q, ws, out)
     pages, page, Hkv = _cache_shape(what, cache)
     shape, dtype = q.shape, q.dtype
-    _need(len(shape) == 3 and shape[2] == HQ_KV4_HEAD, HQ_ERR_SHAPE, what, "q is [Tq, heads, 128]")
-    _need(dtype == torch.bfloat16 or dtype == torch.float16, HQ_ERR_UNSUPPORTED, what, "q's type")
+    if len(shape) != 3 or shape[2] != HQ_KV4_HEAD or (dtype != torch.bfloat16 and dtype != torch.float16):
+        raise HQError(HQ_ERR_UNSUPPORTED if len(shape) == 3 and shape[2] == HQ_KV4_HEAD else HQ_ERR_SHAPE,
+                      what + ": q is BF16 or FP16 [Tq, heads, 128]")
     Tq, Hq, _ = shape
     qs = _heads(what, "q", q, shape, dtype)
     os = (Hq * HQ_KV4_HEAD, HQ_KV4_HEAD) if out is None else _heads(what, "out", out, shape, dtype)
     B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
-    width = block_table.shape[-1] if block_table.dim() == 2 else -1
-    for name, t, n in (("block_table", block_table, (B, width)), ("seq_lens", seq_lens, (B,)), ("cu_q", cu_q, (B + 1,))):
-        if t is None:
-            continue
-        if t.shape != n or not t.is_contiguous():
-            raise HQError(HQ_ERR_SHAPE, f"{what}: {name}'s shape")
-        if t.dtype != torch.int32:
-            raise HQError(HQ_ERR_UNSUPPORTED, f"{what}: {name}'s type")
+    width = _table(what, block_table, B)
+    _vector(what, "seq_lens", seq_lens, B, torch.int32)
+    if cu_q is not None:
+        _vector(what, "cu_q", cu_q, B + 1, torch.int32)
 
     def call(s):
         o = q.new_empty(shape) if out is None else out
