@@ -12,8 +12,8 @@
 //  * K codes are widened to FP16 (exact) and multiplied unscaled; each block's
 //    FP32 product is scaled by its token's E4M3 block scale as it is added up.
 //    q is split into two FP16 parts (hi + lo, 22 bits), so scores are FP32-like.
-//  * for V the weights are scaled instead: P (FP16) times the tokens' block
-//    scales of that block, half as many multiplications as V's codes.
+//  * V's codes, widened and paired by token, times their block scales are exact
+//    in FP16 too (6 significant bits); the weights P are rounded to FP16 once.
 // The cache's byte order gives each lane its operands of a group as 16-byte
 // pieces (four for the codes, three for the block scales).  A warp takes one
 // or two groups (a unit) at a time, copied into its own ring by bulk copies that
@@ -225,11 +225,11 @@ __device__ __forceinline__ void rotate_warp(float (&y)[4], int lane) {
 template <int NT, int W> struct AttnShared {
     static constexpr int NC = 8 * NT, OS = 132;  // columns; padded row of the merge buffer (free of bank conflicts)
     alignas(128) uint8_t ring[W][ATTN_STAGES][2 * KV_GROUP_BYTES];
-    union {
-        float o[W / 2][NC][OS];           // results of the lower half's warps
+    union {  // one after the other within a row
+        uint4 q[NT][8][32];               // per block and lane: hi and lo parts of its four elements of column lane / 4
         float4 frag[W / 2][NT * 8][32];   // accumulators of the upper half's warps
+        float o[W / 2][NC][OS];           // results of the lower half's warps
     };
-    uint4 q[NT][8][32];  // per block and lane: hi and lo parts of its four elements of column lane / 4
     float m[W][NC], l[W][NC];
     float qs[NC];  // factor of a column's scores, in powers of two
     int pos[NC];   // a column's position
@@ -387,11 +387,12 @@ __device__ __forceinline__ void attn_values(const uint8_t* grp, AttnState<NT>& a
         e4m3x4_to_f16(fw1[2 * q + 1], x1[2], x1[3]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const uint32_t a0 = __byte_perm(ea[k], oa[k], 0x5410), a1 = __byte_perm(ea[k], oa[k], 0x7632);
-            const uint32_t a2 = __byte_perm(eb[k], ob[k], 0x5410), a3 = __byte_perm(eb[k], ob[k], 0x7632);
+            const uint32_t a0 = hmul2u(__byte_perm(ea[k], oa[k], 0x5410), x0[k]);
+            const uint32_t a1 = hmul2u(__byte_perm(ea[k], oa[k], 0x7632), x0[k]);
+            const uint32_t a2 = hmul2u(__byte_perm(eb[k], ob[k], 0x5410), x1[k]);
+            const uint32_t a3 = hmul2u(__byte_perm(eb[k], ob[k], 0x7632), x1[k]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                mma16816(a.o[n][4 * q + k], a0, a1, a2, a3, hmul2u(pb[n][0], x0[k]), hmul2u(pb[n][1], x1[k]));
+            for (int n = 0; n < NT; ++n) mma16816(a.o[n][4 * q + k], a0, a1, a2, a3, pb[n][0], pb[n][1]);
         }
     }
 }
