@@ -249,7 +249,8 @@ template <int NT> struct AttnState {
     float qs[NT][2];
 };
 
-// Scores (in powers of two) of the group at `grp`: rows g, g + 8, columns 2 i, 2 i + 1.
+// Scores (in powers of two) of the group at `grp`: rows g, g + 8, columns 2 i,
+// 2 i + 1.
 template <int NT>
 __device__ __forceinline__ void attn_scores(const uint8_t* grp, const uint4 (*q)[8][32], const AttnState<NT>& a, int lane,
                                             float (&s)[NT][4]) {
@@ -486,65 +487,70 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
     const int groups_shift = p.page_shift - 4;
     const bool small_pages = groups_shift == 0;  // a unit's two groups lie on two pages
     auto own = [](const Walk& k) { return max(k.ja, ATTN_ROW_COST); };
-    int lj = own(lw) + w;     // next unit to load of lw's piece
-    int pg[2] = {-1, -1};     // the pages of its groups (looked up one unit ahead), or -1
-    uint32_t stage_ok = 0;    // bits 2 s, 2 s + 1: stage s holds its groups
     auto unit_of = [](const Walk& k, int j) {
         const int t = j - ATTN_ROW_COST;
         return t < k.r.sink_units ? t : k.r.first_unit + (t - k.r.sink_units);
     };
-    auto settle = [&]() {  // on to the next piece with a unit for this warp
-        if (!lw.live || lj < lw.jb) return;
-        Walk t = lw;
-        while (t.live && lj >= t.jb) {
-            walk_next(p, pre, NC, us, t);
-            lj = own(t) + w;
-        }
-        __syncwarp();
-        if (lane == 0) lw = t;
-        __syncwarp();
-    };
-    auto look_up = [&]() {
-        pg[0] = pg[1] = -1;
+    // Up to 32 of the warp's next units in a piece are looked up at once, one by
+    // each lane, which keeps where its unit lies and starts its copy when its
+    // turn comes; masks tell all lanes which of them have their groups.
+    int lj = own(lw) + w;      // the batch's first unit in lw's piece
+    int turn = 32;             // lane whose unit is loaded next; 32: a new batch
+    int count = 0;             // units of the batch
+    uint32_t has0 = 0, has1 = 0;
+    uint32_t src = 0, src1 = 0;  // the lane's unit: its two groups' numbers in the cache
+    uint32_t stage_ok = 0;     // bits 2 s, 2 s + 1: stage s holds its groups
+    auto batch = [&]() {
+        has0 = has1 = 0;
+        turn = 0;
+        count = 0;
         if (!lw.live) return;
-        const int t = unit_of(lw, lj) << (4 + us), len = lw.r.len;
+        if (lj >= lw.jb) {  // on to the next piece with a unit for this warp
+            Walk t = lw;
+            while (t.live && lj >= t.jb) {
+                walk_next(p, pre, NC, us, t);
+                lj = own(t) + w;
+            }
+            __syncwarp();
+            if (lane == 0) lw = t;
+            __syncwarp();
+            if (!lw.live) return;
+        }
+        count = min(32, (lw.jb - lj + W - 1) / W);
+        const int len = lw.r.len, g0 = unit_of(lw, lj + lane * W) << us;  // first group
+        const bool in0 = lane < count && 16 * g0 < len, in1 = us && lane < count && 16 * g0 + 16 < len;
         const int32_t* const row = p.table + (int64_t)lw.b * p.width;
-        if (t < len) pg[0] = row[t >> p.page_shift];
-        if (us && t + 16 < len) pg[1] = small_pages ? row[(t >> 4) + 1] : pg[0];
+        const int pg0 = in0 ? row[g0 >> groups_shift] : -1;
+        const int pg1 = in1 ? (small_pages ? row[g0 + 1] : pg0) : -1;
+        const bool ok0 = (uint32_t)pg0 < (uint64_t)p.num_pages, ok1 = (uint32_t)pg1 < (uint64_t)p.num_pages;  // (not -1)
+        if (in0 != ok0 || in1 != ok1) p.ws[2] = HQ_ERR_PAGE;
+        const uint32_t page_groups = (uint32_t)p.Hkv << groups_shift, head = (uint32_t)lw.head << groups_shift;
+        src = (uint32_t)pg0 * page_groups + head + ((uint32_t)g0 & ((1u << groups_shift) - 1));
+        src1 = (uint32_t)pg1 * page_groups + head;  // (read with pages of one group only)
+        has0 = __ballot_sync(0xFFFFFFFFu, ok0);
+        has1 = __ballot_sync(0xFFFFFFFFu, ok1);
+        lj += W * count;
     };
-    // load the unit at (lw, lj) into stage st, then look up the next one's pages
+    // load the next unit into stage st
     auto issue = [&](int st) {
-        stage_ok &= ~(3u << (2 * st));
-        if (!lw.live) return;
-        const uint32_t ok = ((uint32_t)pg[0] < (uint64_t)p.num_pages ? 1u : 0u) |
-                            ((uint32_t)pg[1] < (uint64_t)p.num_pages ? 2u : 0u);  // (-1 is no page either)
-        const int at = unit_of(lw, lj) << us;
-        if (ok != 3) {  // behind the request's end, or a bad entry
-            const int len = lw.r.len;
-            if ((!(ok & 1) && 16 * at < len) || (us && !(ok & 2) && 16 * at + 16 < len)) p.ws[2] = HQ_ERR_PAGE;
-        }
-        if (ok && lane == 0) {
-            const uint32_t page_groups = (uint32_t)p.Hkv << groups_shift, head = (uint32_t)lw.head << groups_shift;
+        if (turn >= count) batch();
+        const uint32_t ok = (has0 >> turn & 1u) | (has1 >> turn & 1u) << 1;
+        stage_ok = (stage_ok & ~(3u << (2 * st))) | ok << (2 * st);
+        if (lane == turn && ok) {
             const uint32_t dst = smem_u32(sh.ring[w][st]);
-            const uint8_t* const a = p.cache + ((uint64_t)(uint32_t)pg[0] * page_groups + head +
-                                                ((uint32_t)at & ((1u << groups_shift) - 1))) * KV_GROUP_BYTES;
             mbar_arrive_expect(&sh.full[w][st], ok == 3 ? 2 * KV_GROUP_BYTES : KV_GROUP_BYTES);
-            if (ok == 3 && !small_pages) {
-                bulk_load(dst, a, 2 * KV_GROUP_BYTES, &sh.full[w][st]);
+            const uint8_t* const a = p.cache + (uint64_t)src * KV_GROUP_BYTES;
+            if (!small_pages) {
+                bulk_load(dst, a, ok == 3 ? 2 * KV_GROUP_BYTES : KV_GROUP_BYTES, &sh.full[w][st]);
             } else {
                 if (ok & 1) bulk_load(dst, a, KV_GROUP_BYTES, &sh.full[w][st]);
-                if (ok & 2)  // (pages of one group: the head's group on the second page)
-                    bulk_load(dst + KV_GROUP_BYTES, p.cache + ((uint64_t)(uint32_t)pg[1] * page_groups + head) * KV_GROUP_BYTES,
-                              KV_GROUP_BYTES, &sh.full[w][st]);
+                if (ok & 2)
+                    bulk_load(dst + KV_GROUP_BYTES, p.cache + (uint64_t)src1 * KV_GROUP_BYTES, KV_GROUP_BYTES, &sh.full[w][st]);
             }
         }
-        stage_ok |= ok << (2 * st);
-        lj += W;
-        settle();
-        look_up();
+        ++turn;
     };
-    settle();
-    look_up();
+#pragma unroll 1
     for (int s = 0; s < S; ++s) issue(s);
     int st = 0;
     uint32_t phases = 0;  // bit s: parity of stage s's next completion
@@ -605,59 +611,58 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) a.o[n][b][e] = 0.0f;
         }
-        const int pos_min = sh.pos[0], pos_max = sh.pos[NC - 1];
         a.vmax = a.vinv = 0.0f;
 
         for (int j = own(cw) + w; j < cw.jb; j += W) {
             const int cur = st;
             st = st + 1 == S ? 0 : st + 1;
             const uint32_t ok = stage_ok >> (2 * cur) & 3u;
-            if (!ok) {  // no page: the tokens count as not seen
-                issue(cur);
-                continue;
-            }
-            // a copy ends by itself; the limit (about 2 s) only keeps the wait from being endless
-            if (!mbar_wait_bounded(&sh.full[w][cur], phases >> cur & 1u, 2000000u)) p.ws[2] = HQ_ERR_TIMEOUT;
-            phases ^= 1u << cur;
-            const uint8_t* const unit = sh.ring[w][cur];
-            const int t0 = unit_of(cw, j) << (4 + us);
-            if (ok == 3u && t0 + 31 <= pos_min && (p.window == 0 || pos_max - t0 < p.window || t0 + 31 < p.sinks)) {
-                // every column sees every token
-                float s[2][NT][4], v[2][2];
+            if (ok) {  // (no page: the tokens count as not seen)
+                // a copy ends by itself; the limit (about 2 s) only keeps the wait from being endless
+                if (!mbar_wait_bounded(&sh.full[w][cur], phases >> cur & 1u, 2000000u)) p.ws[2] = HQ_ERR_TIMEOUT;
+                phases ^= 1u << cur;
+                const uint8_t* const unit = sh.ring[w][cur];
+                const int t0 = unit_of(cw, j) << (4 + us);
+                // (read again for every unit: as loop constants they cost the accumulators their registers)
+                const int pos_min = *const_cast<volatile int*>(&sh.pos[0]), pos_max = *const_cast<volatile int*>(&sh.pos[NC - 1]);
+                if (ok == 3u && t0 + 31 <= pos_min && (p.window == 0 || pos_max - t0 < p.window || t0 + 31 < p.sinks)) {
+                    // every column sees every token
+                    float s[2][NT][4], v[2][2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint8_t* grp = unit + h * KV_GROUP_BYTES;
-                    attn_scores<NT>(grp, sh.q, a, lane, s[h]);
-                    v[h][0] = *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g);
-                    v[h][1] = *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g + 32);
-                }
-                attn_grow<NT, 2>(a, s, v);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint8_t* grp = unit + h * KV_GROUP_BYTES;
+                        attn_scores<NT>(grp, sh.q, a, lane, s[h]);
+                        v[h][0] = *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g);
+                        v[h][1] = *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g + 32);
+                    }
+                    attn_grow<NT, 2>(a, s, v);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) attn_values<NT, false>(unit + h * KV_GROUP_BYTES, a, s[h], v[h], 0u, 0u, lane);
-            } else {
+                    for (int h = 0; h < 2; ++h) attn_values<NT, false>(unit + h * KV_GROUP_BYTES, a, s[h], v[h], 0u, 0u, lane);
+                } else {
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    if (!(ok >> h & 1u)) continue;
-                    const uint8_t* grp = unit + h * KV_GROUP_BYTES;
-                    float s[1][NT][4], v[1][2];
-                    attn_scores<NT>(grp, sh.q, a, lane, s[0]);
-                    const int t1 = t0 + 16 * h, ta = t1 + g, tb = ta + 8;
+                    for (int h = 0; h < 2; ++h) {
+                        if (!(ok >> h & 1u)) continue;
+                        const uint8_t* grp = unit + h * KV_GROUP_BYTES;
+                        float s[1][NT][4], v[1][2];
+                        attn_scores<NT>(grp, sh.q, a, lane, s[0]);
+                        const int t1 = t0 + 16 * h, ta = t1 + g, tb = ta + 8;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int q = sh.pos[8 * n + 2 * i4 + k];
-                            if (!(ta <= q && (p.window == 0 || q - ta < p.window || ta < p.sinks))) s[0][n][k] = -INFINITY;
-                            if (!(tb <= q && (p.window == 0 || q - tb < p.window || tb < p.sinks))) s[0][n][2 + k] = -INFINITY;
-                        }
-                    // tokens behind the last query's position may hold anything: their value scales count as zero
-                    v[0][0] = ta > pos_max ? 0.0f : *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g);
-                    v[0][1] = tb > pos_max ? 0.0f : *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g + 32);
-                    const int e = pos_max - t1 - 2 * i4;  // the lane's even token is real if e >= 0, the odd one if e >= 1
-                    const uint32_t keep0 = (e >= 0 ? 0x00FF00FFu : 0u) | (e >= 1 ? 0xFF00FF00u : 0u);
-                    const uint32_t keep1 = (e >= 8 ? 0x00FF00FFu : 0u) | (e >= 9 ? 0xFF00FF00u : 0u);
-                    attn_grow<NT, 1>(a, s, v);
-                    attn_values<NT, true>(grp, a, s[0], v[0], keep0, keep1, lane);
+                            for (int k = 0; k < 2; ++k) {
+                                const int q = sh.pos[8 * n + 2 * i4 + k];
+                                if (!(ta <= q && (p.window == 0 || q - ta < p.window || ta < p.sinks))) s[0][n][k] = -INFINITY;
+                                if (!(tb <= q && (p.window == 0 || q - tb < p.window || tb < p.sinks))) s[0][n][2 + k] = -INFINITY;
+                            }
+                        // tokens behind the last query's position may hold anything: their value scales count as zero
+                        v[0][0] = ta > pos_max ? 0.0f : *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g);
+                        v[0][1] = tb > pos_max ? 0.0f : *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g + 32);
+                        const int e = pos_max - t1 - 2 * i4;  // the lane's even token is real if e >= 0, the odd one if e >= 1
+                        const uint32_t keep0 = (e >= 0 ? 0x00FF00FFu : 0u) | (e >= 1 ? 0xFF00FF00u : 0u);
+                        const uint32_t keep1 = (e >= 8 ? 0x00FF00FFu : 0u) | (e >= 9 ? 0xFF00FF00u : 0u);
+                        attn_grow<NT, 1>(a, s, v);
+                        attn_values<NT, true>(grp, a, s[0], v[0], keep0, keep1, lane);
+                    }
                 }
             }
             __syncwarp();  // every lane has read the unit before its stage is filled again

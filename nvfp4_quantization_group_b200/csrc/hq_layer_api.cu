@@ -256,7 +256,7 @@ hq_status hq_kv_slots(int B, const int32_t* lens, const int32_t* new_tokens, int
 size_t hq_kv4_cache_bytes(int64_t num_pages, int page_size, int H) {
     if (page_shift_of(page_size) < 0 || num_pages <= 0 || num_pages > kMaxRows || H <= 0 || H > 65535) return 0;
     const int64_t per_page = (int64_t)H * (page_size / HQ_KV4_GROUP_TOKENS) * HQ_KV4_GROUP_BYTES;
-    if (num_pages > ((int64_t)1 << 50) / per_page) return 0;
+    if (num_pages > ((int64_t)1 << 32) * HQ_KV4_GROUP_BYTES / per_page - 1) return 0;  // groups have 32-bit numbers
     return (size_t)(num_pages * per_page);
 }
 
