@@ -447,7 +447,7 @@ hq_status hq_convert_e2m1_sr(const float *in, const uint8_t *rnd, uint8_t *out, 
  *
  *  dtype      type of x, residual and residual_out; w_dtype: dtype or HQ_DT_F32.
  *  x, residual  [M, K], row strides given; residual NULL: none.
- *  weight     [K].   eps  >= 0.
+ *  weight     [K].   eps  >= 0 (0: a row of zeros has NaN codes).
  *  residual_out [M, K] contiguous: h (needed with a residual, else ignored).
  *             May be x or residual itself where that is contiguous.
  *  out_fp8    uint8 [M, K].
@@ -481,6 +481,7 @@ hq_status hq_add_rmsnorm_fp8_k128(int dtype, const void *x, int64_t x_row_stride
  *  dweight    float [K], or NULL.
  *  ws         >= hq_rmsnorm_backward_workspace_size(M, K) bytes, 16-byte
  *             aligned, any contents (unused without dweight: may be NULL).
+ *             Calls that share one must not overlap in time.
  * The sum over the rows is taken in a fixed order: equal inputs give equal
  * bits on one GPU model.  M == 0 gives dweight = 0.
  * Alignment and errors as above, and HQ_ERR_WORKSPACE.
@@ -659,11 +660,13 @@ hq_status hq_kv4_gather(int dtype, const uint8_t *cache, int64_t num_pages, int 
  *  ws         >= hq_kv4_attention_workspace_size() bytes, 16-byte aligned, in
  *             the rest state (hq_workspace_init); the call leaves it so.  Calls
  *             that share one must not overlap in time.
- * A block-table entry outside [0, num_pages) or a seq_len beyond the row's
- * table_width * page_size tokens sets the workspace's error word to HQ_ERR_PAGE
- * (hq_get_error); the tokens without a page count as not seen.
+ * The workspace's error word (hq_get_error) is set to HQ_ERR_PAGE by a block-table
+ * entry outside [0, num_pages) or a seq_len beyond the row's table_width *
+ * page_size tokens (tokens without a page count as not seen), to HQ_ERR_SHAPE by a
+ * request whose rows reach outside [0, Tq) or are more than q_len (those left out
+ * are not written).
  * Arithmetic: scores in FP32 from FP16 keys (exact) and a two-part FP16 query,
- * weights rounded to FP16 for the second product, sums in FP32.  Results do not
+ * weights rounded to FP16 once for the second product, sums in FP32.  Results do not
  * depend on anything but the inputs and the GPU's SM count.
  * Alignment: q, out, cache, ws 16 bytes, strides of q and out multiples of 8.
  * Errors: HQ_ERR_NULL, HQ_ERR_SHAPE (B > HQ_KV_MAX_REQUESTS, Hq not a multiple

@@ -17,14 +17,23 @@
 // The cache's byte order gives each lane its operands of a group as 16-byte
 // pieces (four for the codes, three for the block scales).  A warp takes one
 // or two groups (a unit) at a time, copied into its own ring by bulk copies that
-// run one unit ahead, so warps never wait for one another inside
-// a row; both groups of a unit that every column sees go through one stretch
-// of code.
+// run one unit ahead, so warps never wait for one another inside a row; both
+// groups of a unit that every column sees go through one stretch of code.
 //
 // The running maximum moves only when a score exceeds it by 5 (in powers of
 // two), so the usual group needs no exchange between lanes: weights stay at
-// or below 32, and the decode scales of V, taken relative to the largest seen
-// so far, at or below 1; 32 * 448 is inside FP16.
+// or below 32, and the decode scales of V, folded into them relative to the
+// largest seen so far, at or below 1.
+//
+// Bound: the codes and scales are 152 bytes per token and key/value head, but a
+// group also costs about 390 warp instructions, 64 of them conversions of code
+// pairs at half rate.  32 requests of 8000 to 16384 tokens, 64 query and 8
+// key/value heads: 121 us, 3.9 TB/s (61 % of the measured copy rate); issue slots
+// 60 % busy, ALU 52 %, matrix 29 %; without the loads 120, without the arithmetic
+// 83.  Steps there: one group a turn 166, two 133, look-ups by whole lanes 121.
+// (These matrix instructions, not tcgen05: its operands would have to be widened
+// into shared memory, 4 x the bytes of the codes written and read again, which at
+// 8 columns costs more than the whole loop has.)
 #include "hq_layer.cuh"
 
 namespace hq {
@@ -34,18 +43,18 @@ constexpr int ATTN_STAGES = 2;       // units in flight per warp
 // with a window of 2047 tokens and up to 20 columns take 55 us with 4, 48 with
 // 8, 45 with 12 or 16, 47 with 24.
 constexpr int ATTN_ROW_COST = 16;
-constexpr int ATTN_MAX_CTAS = 1024;  // workspace: CTAs of a launch at most
+constexpr int ATTN_MAX_CTAS = 512;   // workspace: CTAs of a launch at most
 constexpr int ATTN_MAX_NC = 16;
 constexpr int ATTN_PART = ATTN_MAX_NC * (128 + 2);  // floats of one partial result
 constexpr float ATTN_NONE = -1e30f;  // running maximum before any token
 
 // ---------------------------------------------------------------- schedule
-// Units of one or two groups (16 << us tokens, us = 0 or 1) are numbered request by request, then (head, column
-// tile) row by row, then in the order of the tokens.  Each row counts
-// ATTN_ROW_COST units more than it has, in front of them: what starting and
-// ending a row costs.  CTA c of G takes units [U c / G, U (c + 1) / G), a cut
-// in a row's front part (or right behind it) moved to the row's start: about the same load for every
-// CTA whatever the lengths.
+// Units of one or two groups (16 << us tokens, us = 0 or 1) are numbered request
+// by request, then (head, column tile) row by row, then in the order of the
+// tokens.  Each row counts ATTN_ROW_COST units more than it has, in front of them:
+// what starting and ending a row costs.  CTA c of G takes units [U c / G,
+// U (c + 1) / G), a cut in a row's front part (or right behind it) moved to the
+// row's start: about the same load for every CTA whatever the lengths.
 struct Request {
     int q0, nq;       // first row of q, query tokens
     int len;          // tokens (clamped to the block table's row)
@@ -54,13 +63,14 @@ struct Request {
     int sink_units;   // units of the first tokens, before the window's
     int first_unit;   // the window's first unit
     int n;            // units per row, ATTN_ROW_COST among them (no tokens: one more)
-    bool bad;         // the length exceeds the block table's row
+    uint32_t bad;     // what the error word says of it: rows of q that are not there, or a length beyond the table
 };
 
 __device__ __forceinline__ Request attn_request(const AttnParams& p, int b, int nc, int us) {
     Request r;
     const int ut = 16 << us;
     int64_t a = p.cu_q ? p.cu_q[b] : (int64_t)b * p.q_len, e = p.cu_q ? p.cu_q[b + 1] : a + p.q_len;
+    r.bad = a < 0 || e > p.Tq || e - a > p.q_len ? HQ_ERR_SHAPE : 0;
     a = a < 0 ? 0 : a;
     e = e > p.Tq ? p.Tq : e;
     r.q0 = (int)a;
@@ -68,8 +78,8 @@ __device__ __forceinline__ Request attn_request(const AttnParams& p, int b, int 
     const int64_t row = p.width << p.page_shift;
     const int len = p.lens[b];
     r.last = len - 1;
-    r.bad = len > row;
-    r.len = len < 0 ? 0 : (r.bad ? (int)row : len);
+    if (len > row) r.bad = HQ_ERR_PAGE;
+    r.len = len < 0 ? 0 : (len > row ? (int)row : len);
     r.tiles = (r.nq * p.group + nc - 1) / nc;
     // the window's first token (lengths are below 2^30: host check)
     const int64_t first = (int64_t)r.last - r.nq + 1 - p.window + 1;
@@ -412,7 +422,7 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
     // ---- units before each request: units of one group while there are few
     // (latency counts), of two otherwise (fewer turns of the loops)
     Sched sc;
-    bool bad = false;
+    uint32_t bad = 0;
     int us = 0;
     for (;; ++us) {
         unsigned long long carry = 0;
@@ -422,7 +432,7 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
             if (b < p.B) {
                 const Request r = attn_request(p, b, NC, us);
                 v = (unsigned long long)r.tiles * p.Hkv * r.n;
-                bad |= r.bad && r.nq;
+                if (r.bad && (r.nq || r.bad == HQ_ERR_SHAPE)) bad = r.bad;
             }
             unsigned long long s = v;
 #pragma unroll
@@ -447,13 +457,13 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
     }
     fence_mbar_init();
     __syncthreads();
+    if (bad && blockIdx.x == 0) p.ws[2] = bad;
     if (sc.U == 0) return;
     {  // at least one unit per warp of a CTA
         const uint64_t most = (sc.U + W - 1) / W;
         sc.G = most < gridDim.x ? (uint32_t)most : gridDim.x;
     }
     if (blockIdx.x >= sc.G) return;
-    if (bad) p.ws[2] = HQ_ERR_PAGE;  // (every CTA that is not idle reports the same)
 
     // ---- the warp's loads run ahead of its arithmetic, across pieces.  (The
     // pieces' records live in shared memory: they are read once per unit, and in

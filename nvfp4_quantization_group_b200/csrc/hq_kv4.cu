@@ -175,6 +175,10 @@ void launch_slots(const SlotParams& p, int sms, cudaStream_t st) {
 // 8 bytes of values' codes, that lie together in a group.  The tokens of a tile
 // usually fill one group, whose sectors are then written whole.
 constexpr int KV_THREADS = 128;
+// Resident blocks that the registers are capped for: 16384 tokens x 8 heads
+// written and read back take 46 us with 6, 48 uncapped (4 to 5), 54 with 5 or 7,
+// 58 with 8 (spills).
+constexpr int KV_BLOCKS = 6;
 
 struct KvShared {
     // a vector's 32 chunks of four elements, chunk k of thread j (elements 32 j + 4 k ..) at 8 j + ((k + j) & 7); 36
@@ -219,7 +223,7 @@ __device__ __forceinline__ uint8_t* kv_group(const KvParams& p, int64_t s, int h
 
 // Quantizes as hq_cat_rotate_nvfp4, bit for bit: stages in ascending order, the
 // same scales and conversions.  blockIdx.y is the head.
-template <int DT> __global__ void __launch_bounds__(KV_THREADS) kv4_append_kernel(KvParams p) {
+template <int DT> __global__ void __launch_bounds__(KV_THREADS, KV_BLOCKS) kv4_append_kernel(KvParams p) {
     __shared__ KvShared sh;
     __shared__ float2 vr[128];  // per E4M3 code {value, -RN(1 / value)}
     const int tid = threadIdx.x;
@@ -355,7 +359,7 @@ __device__ __forceinline__ void e2m1x4_to_f32(uint32_t c, float& a, float& b, fl
     e = v.y;
 }
 
-template <int DT> __global__ void __launch_bounds__(KV_THREADS) kv4_gather_kernel(KvParams p) {
+template <int DT> __global__ void __launch_bounds__(KV_THREADS, KV_BLOCKS) kv4_gather_kernel(KvParams p) {
     __shared__ KvShared sh;
     const int tid = threadIdx.x, vec = tid >> 2, i = tid & 3, z = vec >> 4, h = blockIdx.y;
     float4* const row = sh.t[vec];
@@ -457,7 +461,7 @@ template <int DT> __global__ void __launch_bounds__(KV_THREADS) kv4_gather_kerne
 }
 
 static dim3 kv_grid(const KvParams& p, int sms) {
-    const int64_t tiles = (p.N + 15) / 16, cap = ((int64_t)sms * 8 + p.H - 1) / p.H;
+    const int64_t tiles = (p.N + 15) / 16, cap = ((int64_t)sms * 2 * KV_BLOCKS + p.H - 1) / p.H;
     return dim3((unsigned)(tiles < cap ? tiles : cap), (unsigned)p.H);
 }
 void launch_append(int dtype, const KvParams& p, int sms, cudaStream_t st) {

@@ -525,8 +525,8 @@ def _check_attention(got, lse, q, cache, table, lens, rows, scale, window, sinks
     # score: |q| |k| bounds the products' sum; a 128-term FP32 chain and the query's two parts: 2^-17 of it
     norms = q.double().norm(dim=-1, keepdim=True) * 16.0 * scale  # |k| < 16: normal data of 128 dimensions
     ds = 2.0 ** -17 * norms
-    # a weight: two FP16 roundings (2^-11 each), the score's error, exp; below FP16's normal range 2^-25 of the largest
-    # weight each, on values below 8 (their rotation back adds up to sqrt(128) of them); the sums in FP32
+    # a weight: one FP16 rounding (2^-11; the bound leaves room for two), the score's error, exp; below FP16's normal range
+    # 2^-25 of the largest weight each, on values below 8 (their rotation back adds up to sqrt(128) of them); the sums in FP32
     n = float(lens.max())
     tol = U[q.dtype] * want.abs() + weight * (2.0 ** -10 + 2.0 ** -13 + 2 * ds) + 1e-6
     tol = tol + n * peak * 2.0 ** -25 * 8 * (11.4 if rotate else 1)
@@ -615,6 +615,56 @@ def test_kv4_attention_bad_pages_are_reported_and_not_read(hq):
     neg = torch.tensor([-3, 64], dtype=torch.int32, device="cuda")
     out, lse = hq.kv4_attention(q, cache, table, neg, ws=ws, want_lse=True)
     assert bool((out[0] == 0).all()) and bool((lse[0] == -math.inf).all())
+
+
+def test_kv4_attention_rows_that_are_not_there_are_reported(hq):
+    g = _gen(53)
+    cache, table, lens = _filled(hq, g, 2, 1, 16, [40, 50], 128)
+    q, ws = _normal(g, 4, 4, 128, dtype=BF16), hq.kv4_attention_workspace()
+    want = hq.kv4_attention(q[:2].contiguous(), cache, table, lens, ws=ws)
+    assert hq.hq_get_error(ws) == 0
+    for cu in ([0, 1, 9], [-3, 1, 2], [0, 1, 4]):  # beyond the rows of q; before them; more than q_len
+        out = torch.full_like(q, 5.0)
+        hq.kv4_attention(q, cache, table, lens, cu_q=torch.tensor(cu, dtype=torch.int32, device="cuda"), q_len=1, ws=ws, out=out)
+        assert hq.hq_get_error(ws) == hq.HQ_ERR_SHAPE, cu
+        assert torch.equal(out[:2], want) and bool((out[2:] == 5.0).all()), cu
+
+
+def test_kv4_attention_graphs_share_a_workspace(hq):
+    """Two captured calls on one workspace, replayed in turn: each leaves it at rest for the other."""
+    g = _gen(54)
+    ws = hq.kv4_attention_workspace()
+    cases = []
+    for lens in ([3000, 10], [700, 4000, 1]):
+        cache, table, t_lens = _filled(hq, g, len(lens), 2, 16, lens, 128)
+        q = _normal(g, len(lens), 8, 128, dtype=BF16)
+        want = hq.kv4_attention(q, cache, table, t_lens, ws=ws)
+        out = torch.empty_like(q)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            hq.kv4_attention(q, cache, table, t_lens, ws=ws, out=out)
+        cases.append((graph, out, want, q, cache, table, t_lens))
+    for _ in range(3):
+        for graph, out, want, *_ in cases:
+            out.fill_(9.0)
+            graph.replay()
+            assert torch.equal(out, want)
+    assert hq.hq_get_error(ws) == 0
+
+
+def test_kv4_attention_columns_do_not_touch_each_other(hq):
+    """NaN and infinite queries stay in their own rows."""
+    g = _gen(55)
+    cache, table, lens = _filled(hq, g, 2, 1, 32, [300, 70], 128)
+    q = _normal(g, 2, 8, 128, dtype=F16)
+    want = hq.kv4_attention(q, cache, table, lens)
+    q[0, 2, 5], q[0, 6, 7], q[1, 0, 0] = math.nan, math.inf, -math.inf
+    out, lse = hq.kv4_attention(q, cache, table, lens, want_lse=True)
+    bad = torch.zeros((2, 8), dtype=torch.bool, device="cuda")
+    bad[0, 2] = bad[0, 6] = bad[1, 0] = True
+    assert torch.equal(out[~bad], want[~bad]) and bool(torch.isfinite(lse[~bad]).all())
+    assert bool(torch.isnan(out[bad]).all())
 
 
 def test_kv4_attention_extreme_scores(hq):
