@@ -63,14 +63,12 @@ struct Request {
     int sink_units;   // units of the first tokens, before the window's
     int first_unit;   // the window's first unit
     int n;            // units per row, ATTN_ROW_COST among them (no tokens: one more)
-    uint32_t bad;     // what the error word says of it: rows of q that are not there, or a length beyond the table
 };
 
 __device__ __forceinline__ Request attn_request(const AttnParams& p, int b, int nc, int us) {
     Request r;
     const int ut = 16 << us;
     int64_t a = p.cu_q ? p.cu_q[b] : (int64_t)b * p.q_len, e = p.cu_q ? p.cu_q[b + 1] : a + p.q_len;
-    r.bad = a < 0 || e > p.Tq || e - a > p.q_len ? HQ_ERR_SHAPE : 0;
     a = a < 0 ? 0 : a;
     e = e > p.Tq ? p.Tq : e;
     r.q0 = (int)a;
@@ -78,7 +76,6 @@ __device__ __forceinline__ Request attn_request(const AttnParams& p, int b, int 
     const int64_t row = p.width << p.page_shift;
     const int len = p.lens[b];
     r.last = len - 1;
-    if (len > row) r.bad = HQ_ERR_PAGE;
     r.len = len < 0 ? 0 : (len > row ? (int)row : len);
     r.tiles = (r.nq * p.group + nc - 1) / nc;
     // the window's first token (lengths are below 2^30: host check)
@@ -88,6 +85,14 @@ __device__ __forceinline__ Request attn_request(const AttnParams& p, int b, int 
     r.sink_units = min((min(p.sinks, lo) + ut - 1) >> (4 + us), r.first_unit);
     r.n = r.nq ? ATTN_ROW_COST + max(1, r.sink_units + ((r.len + ut - 1) >> (4 + us)) - r.first_unit) : 0;
     return r;
+}
+
+// What the error word says of request b: rows of q that are not there, or a
+// length beyond its row of the block table.
+__device__ __forceinline__ uint32_t attn_bad(const AttnParams& p, int b) {
+    const int64_t a = p.cu_q ? p.cu_q[b] : 0, e = p.cu_q ? p.cu_q[b + 1] : 0;
+    if (a < 0 || e > p.Tq || e - a > p.q_len) return HQ_ERR_SHAPE;
+    return p.lens[b] > p.width << p.page_shift && (!p.cu_q || e > a) ? HQ_ERR_PAGE : 0;
 }
 
 // A CTA's walk over its pieces: a piece is a run of units of one row.
@@ -422,7 +427,6 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
     // ---- units before each request: units of one group while there are few
     // (latency counts), of two otherwise (fewer turns of the loops)
     Sched sc;
-    uint32_t bad = 0;
     int us = 0;
     for (;; ++us) {
         unsigned long long carry = 0;
@@ -432,7 +436,6 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
             if (b < p.B) {
                 const Request r = attn_request(p, b, NC, us);
                 v = (unsigned long long)r.tiles * p.Hkv * r.n;
-                if (r.bad && (r.nq || r.bad == HQ_ERR_SHAPE)) bad = r.bad;
             }
             unsigned long long s = v;
 #pragma unroll
@@ -457,7 +460,9 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
     }
     fence_mbar_init();
     __syncthreads();
-    if (bad && blockIdx.x == 0) p.ws[2] = bad;
+    if (blockIdx.x == 0)
+        for (int b = tid; b < p.B; b += 32 * W)
+            if (const uint32_t bad = attn_bad(p, b)) p.ws[2] = bad;
     if (sc.U == 0) return;
     {  // at least one unit per warp of a CTA
         const uint64_t most = (sc.U + W - 1) / W;
