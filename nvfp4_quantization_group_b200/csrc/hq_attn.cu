@@ -63,6 +63,7 @@ struct Request {
     int sink_units;   // units of the first tokens, before the window's
     int first_unit;   // the window's first unit
     int n;            // units per row, ATTN_ROW_COST among them (no tokens: one more)
+    bool bad;         // the length exceeds the block table's row
 };
 
 __device__ __forceinline__ Request attn_request(const AttnParams& p, int b, int nc, int us) {
@@ -76,7 +77,8 @@ __device__ __forceinline__ Request attn_request(const AttnParams& p, int b, int 
     const int64_t row = p.width << p.page_shift;
     const int len = p.lens[b];
     r.last = len - 1;
-    r.len = len < 0 ? 0 : (len > row ? (int)row : len);
+    r.bad = len > row;
+    r.len = len < 0 ? 0 : (r.bad ? (int)row : len);
     r.tiles = (r.nq * p.group + nc - 1) / nc;
     // the window's first token (lengths are below 2^30: host check)
     const int64_t first = (int64_t)r.last - r.nq + 1 - p.window + 1;
@@ -85,14 +87,6 @@ __device__ __forceinline__ Request attn_request(const AttnParams& p, int b, int 
     r.sink_units = min((min(p.sinks, lo) + ut - 1) >> (4 + us), r.first_unit);
     r.n = r.nq ? ATTN_ROW_COST + max(1, r.sink_units + ((r.len + ut - 1) >> (4 + us)) - r.first_unit) : 0;
     return r;
-}
-
-// What the error word says of request b: rows of q that are not there, or a
-// length beyond its row of the block table.
-__device__ __forceinline__ uint32_t attn_bad(const AttnParams& p, int b) {
-    const int64_t a = p.cu_q ? p.cu_q[b] : 0, e = p.cu_q ? p.cu_q[b + 1] : 0;
-    if (a < 0 || e > p.Tq || e - a > p.q_len) return HQ_ERR_SHAPE;
-    return p.lens[b] > p.width << p.page_shift && (!p.cu_q || e > a) ? HQ_ERR_PAGE : 0;
 }
 
 // A CTA's walk over its pieces: a piece is a run of units of one row.
@@ -461,8 +455,12 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
     fence_mbar_init();
     __syncthreads();
     if (blockIdx.x == 0)
-        for (int b = tid; b < p.B; b += 32 * W)
-            if (const uint32_t bad = attn_bad(p, b)) p.ws[2] = bad;
+        for (int b = tid; b < p.B; b += 32 * W) {
+            if (p.cu_q && (p.cu_q[b] < 0 || p.cu_q[b + 1] > p.Tq || (int64_t)p.cu_q[b + 1] - p.cu_q[b] > p.q_len))
+                p.ws[2] = HQ_ERR_SHAPE;
+            const Request r = attn_request(p, b, NC, 0);
+            if (r.bad && r.nq) p.ws[2] = HQ_ERR_PAGE;
+        }
     if (sc.U == 0) return;
     {  // at least one unit per warp of a CTA
         const uint64_t most = (sc.U + W - 1) / W;
