@@ -8,12 +8,11 @@
 // key/value head fill them:
 //   S^T [16 tokens, n] = K [16, 128] q^T     (8 instructions a part of q)
 //   O^T [16 d,      n] += V^T [16 d, 16 t] P^T  (8 instructions, one per 16-element block)
-// A block scale covers exactly one instruction's depth (K) or height (V):
-//  * K codes are widened to FP16 (exact) and multiplied unscaled; each block's
-//    FP32 product is scaled by its token's E4M3 block scale as it is added up.
-//    q is split into two FP16 parts (hi + lo, 22 bits), so scores are FP32-like.
-//  * V's codes, widened and paired by token, times their block scales are exact
-//    in FP16 too (6 significant bits); the weights P are rounded to FP16 once.
+// A code times its block scale has 6 significant bits and lies within FP16's
+// range, subnormals included: both operands are widened exactly.  (A block scale
+// covers exactly one instruction's depth, K, or height, V.)  The decode scales
+// multiply the scores and the weights in FP32.  q is split into two FP16 parts
+// (hi + lo, 22 bits), so scores are FP32-like; the weights P are rounded to FP16.
 // The cache's byte order gives each lane its operands of a group as 16-byte
 // pieces (four for the codes, three for the block scales).  A warp takes one
 // or two groups (a unit) at a time, copied into its own ring by bulk copies that
@@ -28,12 +27,13 @@
 // Bound: the codes and scales are 152 bytes per token and key/value head, but a
 // group also costs about 390 warp instructions, 64 of them conversions of code
 // pairs at half rate.  32 requests of 8000 to 16384 tokens, 64 query and 8
-// key/value heads: 121 us, 3.9 TB/s (61 % of the measured copy rate); issue slots
-// 60 % busy, ALU 52 %, matrix 29 %; without the loads 120, without the arithmetic
-// 83.  Steps there: one group a turn 166, two 133, look-ups by whole lanes 121.
-// (These matrix instructions, not tcgen05: its operands would have to be widened
-// into shared memory, 4 x the bytes of the codes written and read again, which at
-// 8 columns costs more than the whole loop has.)
+// key/value heads: 119 us, 4.0 TB/s (62 % of the measured copy rate); issue slots
+// 60 % busy, ALU 52 %, matrix 29 %; without the loads it takes about 120, without
+// the arithmetic 83.  Steps there: one group a turn 166, two 133, look-ups by
+// whole lanes 121.  (These matrix instructions, not tcgen05: that one reads its
+// operands from shared memory, where K and V would have to be widened first: 512
+// bytes per token and head written and read again, 8 clocks of an SM's shared
+// memory beside the 2.4 of the codes, where the whole loop takes 10.5.)
 #include "hq_layer.cuh"
 
 namespace hq {
@@ -196,7 +196,12 @@ __device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ float2 h2f(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+// A pair times the low (HI: high) half of `f`.
+template <bool HI> __device__ __forceinline__ uint32_t hmul2_half(uint32_t a, uint32_t f) {
+    const __half2 s = *reinterpret_cast<const __half2*>(&f);
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), HI ? __high2half2(s) : __low2half2(s));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -274,32 +279,37 @@ __device__ __forceinline__ void attn_scores(const uint8_t* grp, const uint4 (*q)
     e4m3x4_to_f16(f0.y, sf0[2], sf0[3]);
     e4m3x4_to_f16(f1.x, sf1[0], sf1[1]);
     e4m3x4_to_f16(f1.y, sf1[2], sf1[3]);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
+    // four running products (hi and lo parts, even and odd pairs of blocks): short chains
+    float c[NT][4][4];
 #pragma unroll
     for (int b2 = 0; b2 < 4; ++b2) {  // blocks 2 b2, 2 b2 + 1
         uint32_t a0[4], a1[4];
         e2m1x8_to_f16(kw0[b2], a0);
         e2m1x8_to_f16(kw1[b2], a1);
-        const float2 x0 = h2f(sf0[b2]), x1 = h2f(sf1[b2]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t m0 = k ? hmul2_half<true>(a0[2], sf0[b2]) : hmul2_half<false>(a0[0], sf0[b2]);
+            const uint32_t m1 = k ? hmul2_half<true>(a1[2], sf1[b2]) : hmul2_half<false>(a1[0], sf1[b2]);
+            const uint32_t m2 = k ? hmul2_half<true>(a0[3], sf0[b2]) : hmul2_half<false>(a0[1], sf0[b2]);
+            const uint32_t m3 = k ? hmul2_half<true>(a1[3], sf1[b2]) : hmul2_half<false>(a1[1], sf1[b2]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int n = 0; n < NT; ++n) {
                 const uint4 f = q[n][2 * b2 + k][lane];
-                float c[4];
-                mma16816_first(c, a0[2 * k], a1[2 * k], a0[2 * k + 1], a1[2 * k + 1], f.x, f.y);
-                mma16816(c, a0[2 * k], a1[2 * k], a0[2 * k + 1], a1[2 * k + 1], f.z, f.w);
-                const float y0 = k ? x0.y : x0.x, y1 = k ? x1.y : x1.x;
-                s[n][0] = __fmaf_rn(y0, c[0], s[n][0]);
-                s[n][1] = __fmaf_rn(y0, c[1], s[n][1]);
-                s[n][2] = __fmaf_rn(y1, c[2], s[n][2]);
-                s[n][3] = __fmaf_rn(y1, c[3], s[n][3]);
+                const int z = 2 * (b2 & 1);
+                if (b2 < 2 && k == 0) {
+                    mma16816_first(c[n][z], m0, m1, m2, m3, f.x, f.y);
+                    mma16816_first(c[n][z + 1], m0, m1, m2, m3, f.z, f.w);
+                } else {
+                    mma16816(c[n][z], m0, m1, m2, m3, f.x, f.y);
+                    mma16816(c[n][z + 1], m0, m1, m2, m3, f.z, f.w);
+                }
             }
         }
     }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = (c[n][0][e] + c[n][2][e]) + (c[n][1][e] + c[n][3][e]);
     const float d0 = *reinterpret_cast<const float*>(grp + KV_K_DEC + 4 * g);
     const float d1 = *reinterpret_cast<const float*>(grp + KV_K_DEC + 4 * g + 32);
 #pragma unroll
