@@ -40,8 +40,8 @@ namespace hq {
 
 constexpr int ATTN_STAGES = 2;       // units in flight per warp
 // Units that a row's start and end (its q, the joins) are worth: 48 requests
-// with a window of 2047 tokens and up to 20 columns take 55 us with 4, 48 with
-// 8, 45 with 12 or 16, 47 with 24.
+// with a window of 2047 tokens and up to 20 columns take 47 us with 8, 40 with
+// 12, 37 with 16 or 24.
 constexpr int ATTN_ROW_COST = 16;
 constexpr int ATTN_MAX_CTAS = 512;   // workspace: CTAs of a launch at most
 constexpr int ATTN_MAX_NC = 16;
@@ -846,10 +846,10 @@ template <int DT, int NT, int W, int MINB> static int launch_t(const AttnParams&
 }
 
 int launch_attn(int dtype, const AttnParams& p, int sms, cudaStream_t st) {
-    // Two column tiles of 8 in one pass cost about 1.8 times one (measured at
-    // 16 requests of 8000 to 16000 tokens: 16 columns 66 us against 72 in two
-    // passes, 12 columns 64 against 71; 20 columns, three tiles, 45 against 38),
-    // so they are paired when their number is even.
+    // Two column tiles of 8 in one pass cost about 1.8 times one (16 requests of
+    // 8000 to 16000 tokens: 16 columns 60 us against 65 one by one, 32 columns 95
+    // against 114; up to 20 columns, three tiles, 43 against 37 where they leave
+    // half a pass empty), so they are paired when their number is even.
     const bool wide = ((int64_t)p.q_len * p.group + 7) / 8 % 2 == 0;
     if (dtype == HQ_DT_BF16)
         return wide ? launch_t<HQ_DT_BF16, 2, 4, 2>(p, sms, st) : launch_t<HQ_DT_BF16, 1, 8, 2>(p, sms, st);
