@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv_slots_kernel(SlotParams p, in
     int* const cu = need + p.B + 1;
     int* const lens = cu + p.B + 1;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, P = 1 << p.page_shift;
+    let_next();  // (one block: the rest of the GPU is free for kv_slot_rows_kernel's)
     const long long row_tokens = p.width << p.page_shift;
     const long long count = *p.count;
     if (tid == 0) {
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv_slots_kernel(SlotParams p, in
 // left sums of zero: no row is in use).
 __global__ void __launch_bounds__(256) kv_slot_rows_kernel(SlotParams p) {
     extern __shared__ __align__(16) int sums[];  // [B + 1]
+    after_previous();
     for (int b = threadIdx.x; b <= p.B; b += 256) sums[b] = p.cu[b];
     __syncthreads();
     const int total = sums[p.B], P = 1 << p.page_shift;
@@ -163,7 +165,8 @@ void launch_slots(const SlotParams& p, int sms, cudaStream_t st) {
     kv_slots_kernel<<<1, SLOT_THREADS, bytes(p.B), st>>>(p, rows ? 0 : (int)p.n_slots);
     if (rows) {
         const int64_t blocks = (p.n_slots + 1023) / 1024, cap = 2 * (int64_t)sms;
-        kv_slot_rows_kernel<<<(unsigned)(blocks < cap ? blocks : cap), 256, sizeof(int) * ((size_t)p.B + 1), st>>>(p);
+        launch_next(kv_slot_rows_kernel, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256),
+                    sizeof(int) * ((size_t)p.B + 1), st, p);
     }
 }
 

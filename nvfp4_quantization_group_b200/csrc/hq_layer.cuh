@@ -149,6 +149,27 @@ __device__ __forceinline__ uint2 fp8_codes8(const float (&y)[8], float s) {
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
+// A kernel of the same call that follows another one: its blocks may be placed
+// while the first one's last blocks run, and wait for its end (and its writes)
+// in after_previous().  The first kernel says let_next() where it no longer
+// matters when the next one's blocks take room.
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+void launch_next(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid;
+    c.blockDim = block;
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    c.attrs = at;
+    c.numAttrs = 1;
+    cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+}
+
 // Lets a kernel use `bytes` of dynamic shared memory on the current device;
 // asked once per kernel and device.  Returns a cudaError_t.
 template <typename K> int allow_shared(K* kernel, size_t bytes) {

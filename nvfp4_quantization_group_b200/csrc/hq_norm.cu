@@ -225,6 +225,7 @@ __global__ void __launch_bounds__(T, MINB) rmsnorm_back_kernel(NormBackParams p)
         load(m + step);
     }
     if (!p.dw) return;
+    let_next();
     float* const part = p.partial + (int64_t)blockIdx.x * p.K;
     if constexpr (WARP) {
         for (int x = 0; x < (int)blockDim.x / 32; ++x) {  // the warps in order
@@ -269,12 +270,22 @@ template <int DT> __global__ void __launch_bounds__(256) rmsnorm_dw_kernel(NormB
 }
 
 // Sum of `parts` rows of partial sums: 32 columns a block, thread row y takes
-// rows y, y + 32, ..., then the 32 of them in order.
+// rows y, y + 32, ... (eight of them in flight), then the 32 of them in order.
 __global__ void __launch_bounds__(1024) rmsnorm_dw_join_kernel(const float* partial, float* dw, int64_t K, int parts) {
     __shared__ float s[32][33];
     const int64_t k = (int64_t)blockIdx.x * 32 + threadIdx.x;
     float a = 0.0f;
-    for (int r = threadIdx.y; r < parts; r += 32) a = __fadd_rn(a, partial[(int64_t)r * K + k]);
+    after_previous();
+    for (int r0 = threadIdx.y; r0 < parts; r0 += 32 * 8) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = r0 + 32 * j;
+            v[j] = r < parts ? __ldcg(partial + (int64_t)r * K + k) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a = __fadd_rn(a, v[j]);
+    }
     s[threadIdx.y][threadIdx.x] = a;
     __syncthreads();
     const float b = warp_sum(s[threadIdx.x][threadIdx.y]);  // column y's 32 sums
@@ -324,7 +335,7 @@ template <int DT, int WDT> static void norm_back_t(const NormBackParams& p, int 
         q.dw = nullptr;
         norm_back_launch<DT, WDT, 8, 1024, 1, false>(q, block(8), sms, st);
     }
-    if (p.dw) rmsnorm_dw_join_kernel<<<(unsigned)(p.K / 32), dim3(32, 32), 0, st>>>(p.partial, p.dw, p.K, parts);
+    if (p.dw) launch_next(rmsnorm_dw_join_kernel, dim3((unsigned)(p.K / 32)), dim3(32, 32), 0, st, p.partial, p.dw, p.K, parts);
 }
 void launch_norm_back(int dtype, int w_dtype, const NormBackParams& p, int sms, cudaStream_t st) {
     const bool wf = w_dtype == HQ_DT_F32;
