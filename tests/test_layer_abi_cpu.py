@@ -4,9 +4,14 @@ from __future__ import annotations
 
 import ctypes
 import math
+import os
+import re
 
+import numpy as np
 import pytest
 import torch
+
+import _kv4
 
 import nvfp4_quantization_group_b200 as hq
 
@@ -244,3 +249,29 @@ def test_conveniences_refuse_before_any_launch():
     assert hq.kv4_cache(4, 32, 2, device="cpu").shape == (4, 2, 2, hq.HQ_KV4_GROUP_BYTES)
     with pytest.raises(hq.HQError):
         hq.rmsnorm_backward_workspace(4, 100, device="cpu")
+
+
+def test_cache_layout_of_the_document():
+    """FORMAT.md's offsets fill a group's 2432 bytes exactly once and are those that the GPU tests read with."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "FORMAT.md")
+    text = open(path, encoding="utf-8").read()
+    part = text[text.index("### 6.5 "):]
+    rows = dict(re.findall(r"^\| ([KV][a-z ]+?)(?: \(float\))? \| [^|]+ \| `([^`]+)` \|$", part[:part.index("## 7.")], flags=re.M))
+    assert len(rows) == 6
+    used = np.zeros(hq.HQ_KV4_GROUP_BYTES, int)
+    group = np.arange(hq.HQ_KV4_GROUP_BYTES) % 251
+    group = group.astype(np.uint8)
+    for value, name in ((False, "K"), (True, "V")):
+        at = lambda what, r, j=0: eval(rows[f"{name} {what}"], {"__builtins__": {}}, {"r": r, "j": j})  # noqa: E731
+        for r in range(16):
+            codes, sf, dec = _kv4.token_bytes(group, r, value)
+            for j in range(0, 128, 2):
+                used[at("codes", r, j)] += 1
+                assert group[at("codes", r, j)] == codes[j // 2]
+            for j in range(0, 128, 16):
+                used[at("block scales", r, j)] += 1
+                assert group[at("block scales", r, j)] == sf[j // 16]
+            first = at("decode scale", r)
+            used[first:first + 4] += 1
+            assert group[first:first + 4].view(np.float32)[0] == dec
+    assert (used == 1).all()
