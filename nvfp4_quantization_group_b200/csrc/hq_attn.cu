@@ -661,7 +661,8 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                     attn_grow<NT, 2>(a, s, v);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) attn_values<NT, false>(unit + h * KV_GROUP_BYTES, a, s[h], v[h], 0u, 0u, lane);
-                } else {
+                } else if (t0 <= pos_max && !(p.window > 0 && t0 + 31 <= pos_min - p.window && t0 >= p.sinks)) {
+                    // some do (in a chunk of a prefill, a unit may be ahead of all of these columns, or behind their window)
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         if (!(ok >> h & 1u)) continue;

@@ -767,3 +767,92 @@ def test_calls_on_another_stream(hq):
         side.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------------- sizes and neighbours
+def test_kv4_attention_of_many_requests(hq):
+    """More requests than a block has threads, most of them tiny, some empty."""
+    g = _gen(81)
+    B, page = 3001, 16
+    lens = torch.randint(0, 40, (B,), generator=torch.Generator().manual_seed(5)).tolist()
+    lens[1234] = 2000
+    cache, table, t_lens = _filled(hq, g, B, 1, page, lens, 128)
+    q = _normal(g, B, 4, 128, dtype=BF16)
+    out, lse = hq.kv4_attention(q, cache, table, t_lens, want_lse=True)
+    for b in list(range(0, B, 211)) + [1233, 1234, 1235, B - 1]:
+        rows = [(0, 0)] * b + [(b, b + 1)] + [(0, 0)] * (B - b - 1)
+        want, lse64, weight, _ = attention64(q, cache, table, lens, rows, 128 ** -0.5, 0, 0, True)
+        tol = U[BF16] * want[b].abs() + weight[b] * (2.0 ** -10 + 2.0 ** -12) + 1e-5  # as in _check_attention
+        assert bool(((out[b].double() - want[b]).abs() <= tol).all()), b
+        if lens[b]:
+            assert bool(((lse[b].double() - lse64[b]).abs() < 1e-3).all()), b
+    empty = t_lens == 0
+    assert bool((out[empty] == 0).all()) and bool((lse[empty] == -math.inf).all())
+
+
+def test_kv4_cache_beyond_32_bit_offsets(hq):
+    """Pages whose bytes lie behind 2^32: the same results as in a small cache."""
+    g = _gen(82)
+    H, page, pages = 8, 64, 60_000  # 4.7 GB
+    big = torch.empty((pages, H, page // 16, 2432), dtype=torch.uint8, device="cuda")
+    small = hq.kv4_cache(4, page, H)
+    n = 200
+    k, v = _normal(g, n, H, 128, dtype=BF16), _normal(g, n, H, 128, dtype=BF16)
+    where = torch.tensor([pages - 1, pages - 3, 57_000, pages - 2], device="cuda")
+    t = torch.arange(n, device="cuda")
+    hq.kv4_append(k, v, t, small)
+    hq.kv4_append(k, v, where[t // page] * page + t % page, big)
+    assert torch.equal(hq.kv4_gather(small, t)[0], hq.kv4_gather(big, where[t // page] * page + t % page)[0])
+    q, lens = _normal(g, 1, 4 * H, 128, dtype=BF16), torch.tensor([n], dtype=torch.int32, device="cuda")
+    a = hq.kv4_attention(q, small, torch.arange(4, dtype=torch.int32, device="cuda")[None], lens)
+    assert torch.equal(a, hq.kv4_attention(q, big, where.to(torch.int32)[None], lens))
+
+
+def test_norm_and_rope_beyond_32_bit_offsets(hq):
+    """Tensors of more than 2^31 elements: the last rows as in a call on them alone."""
+    g = _gen(83)
+    M, K = 70_001, 32_768
+    x = torch.zeros((M, K), dtype=BF16, device="cuda")
+    x[-3:] = _normal(g, 3, K, dtype=BF16)
+    w = _normal(g, K, dtype=BF16)
+    out, last = hq.add_rmsnorm_fp8_k128(x, w, want_rstd=True), hq.add_rmsnorm_fp8_k128(x[-3:].contiguous(), w, want_rstd=True)
+    for name in last:
+        assert torch.equal(out[name][-3:], last[name]), name
+    rstd = out["rstd"]
+    del out
+    dx, dw = hq.rmsnorm_backward(x, x, w, rstd)
+    dx3, dw3 = hq.rmsnorm_backward(x[-3:].contiguous(), x[-3:].contiguous(), w, rstd[-3:].contiguous())
+    assert torch.equal(dx[-3:], dx3) and torch.equal(dw, dw3)  # (the other rows add zeros)
+    del dx
+    q = x.view(M, 256, 128)
+    pos, (inv, _) = torch.arange(M, device="cuda"), hq.rope_inv_freq(128)
+    y, _ = hq.rope(q, None, pos, inv)
+    assert torch.equal(y[-3:], hq.rope(q[-3:].contiguous(), None, pos[-3:].contiguous(), inv)[0])
+
+
+def test_calls_on_two_streams_at_once(hq):
+    """Calls that share no workspace do not disturb each other."""
+    g = _gen(84)
+    streams, sets = [torch.cuda.Stream() for _ in range(2)], []
+    for k in range(2):
+        cache, table, lens = _filled(hq, g, 3, 2, 32, [900 + 500 * k, 33, 2000], 128)
+        sets.append((_normal(g, 3, 8, 128, dtype=BF16), cache, table, lens, hq.kv4_attention_workspace(),
+                     _normal(g, 300, 1024, dtype=BF16), _normal(g, 1024, dtype=BF16), hq.rmsnorm_backward_workspace(300, 1024)))
+    rstd = torch.ones(300, device="cuda")
+
+    def calls(s):
+        q, cache, table, lens, ws, x, w, ws2 = s
+        return [hq.kv4_attention(q, cache, table, lens, ws=ws), *hq.rmsnorm_backward(x, x, w, rstd, ws=ws2)]
+
+    want = [calls(s) for s in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(calls(sets[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for outs in got[k]:
+            for a, b in zip(outs, want[k]):
+                assert torch.equal(a, b)
