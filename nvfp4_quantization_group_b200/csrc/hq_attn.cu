@@ -27,7 +27,7 @@
 // Bound: the codes and scales are 152 bytes per token and key/value head, but a
 // group also costs about 390 warp instructions, 64 of them conversions of code
 // pairs at half rate.  32 requests of 8000 to 16384 tokens, 64 query and 8
-// key/value heads: 119 us, 4.0 TB/s (62 % of the measured copy rate); issue slots
+// key/value heads: 118 us, 4.0 TB/s (62 % of the measured copy rate); issue slots
 // 60 % busy, ALU 52 %, matrix 29 %; without the loads it takes about 120, without
 // the arithmetic 83.  Steps there: one group a turn 166, two 133, look-ups by
 // whole lanes 121.  (These matrix instructions, not tcgen05: that one reads its
@@ -484,8 +484,10 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
     Walk& cw = sh.cw;
     Walk& lw = sh.lw[w];
     {
+        // (lanes 0 and 1 find the two ends side by side)
+        const uint64_t end = cta_first(p, pre, NC, us, sc, blockIdx.x + (lane & 1));
         Walk t;
-        walk_start(p, pre, NC, us, cta_first(p, pre, NC, us, sc, blockIdx.x), cta_first(p, pre, NC, us, sc, blockIdx.x + 1), t);
+        walk_start(p, pre, NC, us, __shfl_sync(0xFFFFFFFFu, end, 0), __shfl_sync(0xFFFFFFFFu, end, 1), t);
         if (tid == 0) cw = t;
         if (lane == 0) lw = t;
     }
@@ -809,17 +811,30 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                 __threadfence();
                 for (int c = w; c < tile_cols; c += W) {
                     float mx = ATTN_NONE, L = 0.0f, y[4] = {};
-                    for (uint32_t k = first; k <= last; ++k) {
-                        const float* part = parts + (size_t)(2 * k + (k == first ? 1 : 0)) * ATTN_PART;
-                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part + ATTN_MAX_NC * 128 + 2 * c));
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(part + c * 128 + 4 * lane));
-                        const float t = fmaxf(mx, ml.x), fa = ex2(mx - t), fb = ex2(ml.x - t);
-                        mx = t;
-                        L = L * fa + ml.y * fb;
-                        y[0] = y[0] * fa + v.x * fb;
-                        y[1] = y[1] * fa + v.y * fb;
-                        y[2] = y[2] * fa + v.z * fb;
-                        y[3] = y[3] * fa + v.w * fb;
+                    for (uint32_t k0 = first; k0 <= last; k0 += 4) {  // four results on their way at a time
+                        float2 ml[4];
+                        float4 v[4];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const uint32_t k = k0 + z;
+                            const float* part = parts + (size_t)(2 * k + (k == first ? 1 : 0)) * ATTN_PART;
+                            ml[z] = make_float2(ATTN_NONE, 0.0f);
+                            v[z] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (k <= last) {
+                                ml[z] = __ldcg(reinterpret_cast<const float2*>(part + ATTN_MAX_NC * 128 + 2 * c));
+                                v[z] = __ldcg(reinterpret_cast<const float4*>(part + c * 128 + 4 * lane));
+                            }
+                        }
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const float t = fmaxf(mx, ml[z].x), fa = ex2(mx - t), fb = ex2(ml[z].x - t);
+                            mx = t;
+                            L = L * fa + ml[z].y * fb;
+                            y[0] = y[0] * fa + v[z].x * fb;
+                            y[1] = y[1] * fa + v[z].y * fb;
+                            y[2] = y[2] * fa + v[z].z * fb;
+                            y[3] = y[3] * fa + v[z].w * fb;
+                        }
                     }
                     store(c, y, mx, L);
                 }
