@@ -1,7 +1,9 @@
 """Build the hq CUDA library in-tree: nvfp4_quantization_group_b200/libhq.so.
 
 nvcc compiles every csrc/*.cu for sm_100a only; the result is a plain shared
-library exporting the extern "C" entry points declared in include/hq.h.
+library exporting the extern "C" entry points declared in include/hq.h.  Beside
+it _hq_torch.so (csrc/hq_torch.cpp, host code only): the conveniences of
+layer.py on torch tensors, which call those entry points.
 """
 from __future__ import annotations
 
@@ -16,6 +18,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libhq.so")
+TORCH_SRC = os.path.join(CSRC, "hq_torch.cpp")
+TORCH_LIB = os.path.join(PKG, "_hq_torch.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 NVCC_FLAGS = [
@@ -47,8 +51,32 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_torch(force: bool = False) -> str:
+    """Compile the torch-tensor conveniences (when their source changed) and return their path."""
+    deps = [TORCH_SRC, os.path.join(INCLUDE, "hq.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(TORCH_LIB) and all(os.path.getmtime(d) <= os.path.getmtime(TORCH_LIB) for d in deps):
+        return TORCH_LIB
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    include = [*include_paths(), os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    tmp = TORCH_LIB + f".{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(x for i in include for x in ("-I", i)),
+           TORCH_SRC, "-o", tmp, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-lc10_cuda", "-ltorch",
+           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {TORCH_SRC}:\n{r.stdout}{r.stderr}")
+    os.replace(tmp, TORCH_LIB)
+    return TORCH_LIB
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (when sources changed) and return the library path."""
+    build_torch(force)
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
