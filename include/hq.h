@@ -666,7 +666,8 @@ hq_status hq_kv4_gather(int dtype, const uint8_t *cache, int64_t num_pages, int 
  * request whose rows reach outside [0, Tq) or are more than q_len (those left out
  * are not written).
  * Arithmetic: scores in FP32 from FP16 keys (exact) and a two-part FP16 query,
- * weights rounded to FP16 once for the second product, sums in FP32.  Results do not
+ * weights rounded to FP16 (BF16 outputs) or in two FP16 parts (FP16 outputs) for
+ * the second product, sums in FP32.  Results do not
  * depend on anything but the inputs and the GPU's SM count.
  * Alignment: q, out, cache, ws 16 bytes, strides of q and out multiples of 8.
  * Errors: HQ_ERR_NULL, HQ_ERR_SHAPE (B > HQ_KV_MAX_REQUESTS, Hq not a multiple

@@ -12,7 +12,10 @@
 // range, subnormals included: both operands are widened exactly.  (A block scale
 // covers exactly one instruction's depth, K, or height, V.)  The decode scales
 // multiply the scores and the weights in FP32.  q is split into two FP16 parts
-// (hi + lo, 22 bits), so scores are FP32-like; the weights P are rounded to FP16.
+// (hi + lo, 22 bits), so scores are FP32-like.  The weights P are rounded to FP16
+// once for BF16 outputs, whose own rounding is eight times as coarse; for FP16
+// outputs they too go in two parts (the error against 64 bits is then the output's
+// own, 2.1e-4, where one part gives 2.9e-4; 118 -> 127 us at the sizes below).
 // The cache's byte order gives each lane its operands of a group as 16-byte
 // pieces (four for the codes, three for the block scales).  A warp takes one
 // or two groups (a unit) at a time, copied into its own ring by bulk copies that
@@ -202,6 +205,7 @@ template <bool HI> __device__ __forceinline__ uint32_t hmul2_half(uint32_t a, ui
     const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), HI ? __high2half2(s) : __low2half2(s));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
+__device__ __forceinline__ float2 h2f(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -370,7 +374,7 @@ __device__ __forceinline__ void attn_grow(AttnState<NT>& a, const float (&s)[N][
 // Adds the group's weighted values.  v: decode scales of rows g, g + 8; keep0,
 // keep1: the bytes to keep of the block scales of the lane's tokens 2 i, 2 i + 1
 // and 2 i + 8, + 9.
-template <int NT, bool MASK>
+template <int NT, bool MASK, bool FINE>
 __device__ __forceinline__ void attn_values(const uint8_t* grp, AttnState<NT>& a, const float (&s)[NT][4],
                                             const float (&v)[2], uint32_t keep0, uint32_t keep1, int lane) {
     const float r0 = v[0] * a.vinv, r1 = v[1] * a.vinv;
@@ -380,15 +384,22 @@ __device__ __forceinline__ void attn_values(const uint8_t* grp, AttnState<NT>& a
         vf0 = make_uint4(vf0.x & keep0, vf0.y & keep0, vf0.z & keep0, vf0.w & keep0);
         vf1 = make_uint4(vf1.x & keep1, vf1.y & keep1, vf1.z & keep1, vf1.w & keep1);
     }
-    uint32_t pb[NT][2];  // weights as the n side: column g, tokens 2 i, 2 i + 1 and 2 i + 8, + 9
+    uint32_t pb[NT][2], pl[NT][2];  // weights as the n side: column g, tokens 2 i, 2 i + 1 and 2 i + 8, + 9; FINE: their rest
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const float e0 = ex2(s[n][0] - a.m[n][0]), e1 = ex2(s[n][1] - a.m[n][1]);
         const float e2 = ex2(s[n][2] - a.m[n][0]), e3 = ex2(s[n][3] - a.m[n][1]);
         a.l[n][0] += e0 + e2;
         a.l[n][1] += e1 + e3;
-        pb[n][0] = transpose8x8(pack_h2(e0 * r0, e1 * r0));
-        pb[n][1] = transpose8x8(pack_h2(e2 * r1, e3 * r1));
+        const float w0 = e0 * r0, w1 = e1 * r0, w2 = e2 * r1, w3 = e3 * r1;
+        const uint32_t u = pack_h2(w0, w1), v2 = pack_h2(w2, w3);
+        pb[n][0] = transpose8x8(u);
+        pb[n][1] = transpose8x8(v2);
+        if constexpr (FINE) {
+            const float2 a0 = h2f(u), a1 = h2f(v2);
+            pl[n][0] = transpose8x8(pack_h2(w0 - a0.x, w1 - a0.y));
+            pl[n][1] = transpose8x8(pack_h2(w2 - a1.x, w3 - a1.y));
+        }
     }
     const uint4 c0 = *reinterpret_cast<const uint4*>(grp + KV_V_CODES + lane * 16);
     const uint4 c1 = *reinterpret_cast<const uint4*>(grp + KV_V_CODES + lane * 16 + 512);
@@ -412,7 +423,10 @@ __device__ __forceinline__ void attn_values(const uint8_t* grp, AttnState<NT>& a
             const uint32_t a2 = hmul2u(__byte_perm(eb[k], ob[k], 0x5410), x1[k]);
             const uint32_t a3 = hmul2u(__byte_perm(eb[k], ob[k], 0x7632), x1[k]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(a.o[n][4 * q + k], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+            for (int n = 0; n < NT; ++n) {
+                mma16816(a.o[n][4 * q + k], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                if constexpr (FINE) mma16816(a.o[n][4 * q + k], a0, a1, a2, a3, pl[n][0], pl[n][1]);
+            }
         }
     }
 }
@@ -422,6 +436,7 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
     typedef typename Elem<DT>::T T;
     typedef AttnShared<NT, W> Shared;
     constexpr int NC = 8 * NT, S = ATTN_STAGES;
+    constexpr bool FINE = DT == HQ_DT_F16;  // weights in two parts
     extern __shared__ __align__(128) uint8_t raw[];
     Shared& sh = *reinterpret_cast<Shared*>(raw);
     uint64_t* const pre = reinterpret_cast<uint64_t*>(raw + sizeof(Shared));
@@ -662,7 +677,7 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                     }
                     attn_grow<NT, 2>(a, s, v);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) attn_values<NT, false>(unit + h * KV_GROUP_BYTES, a, s[h], v[h], 0u, 0u, lane);
+                    for (int h = 0; h < 2; ++h) attn_values<NT, false, FINE>(unit + h * KV_GROUP_BYTES, a, s[h], v[h], 0u, 0u, lane);
                 } else if (t0 <= pos_max && !(p.window > 0 && t0 + 31 <= pos_min - p.window && t0 >= p.sinks)) {
                     // some do (in a chunk of a prefill, a unit may be ahead of all of these columns, or behind their window)
 #pragma unroll 1
@@ -687,7 +702,7 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                         const uint32_t keep0 = (e >= 0 ? 0x00FF00FFu : 0u) | (e >= 1 ? 0xFF00FF00u : 0u);
                         const uint32_t keep1 = (e >= 8 ? 0x00FF00FFu : 0u) | (e >= 9 ? 0xFF00FF00u : 0u);
                         attn_grow<NT, 1>(a, s, v);
-                        attn_values<NT, true>(grp, a, s[0], v[0], keep0, keep1, lane);
+                        attn_values<NT, true, FINE>(grp, a, s[0], v[0], keep0, keep1, lane);
                     }
                 }
             }
