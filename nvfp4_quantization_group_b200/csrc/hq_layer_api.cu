@@ -191,8 +191,9 @@ hq_status hq_rope(int dtype, const void* q, int64_t q_token_stride, int64_t q_he
     const int sms = device_sms();
     if (!sms) return HQ_ERR_CUDA;
     RopeParams p;
-    p.t[0] = RopeTensor{q, q_out, q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride, Hq};
-    p.t[1] = RopeTensor{k, k_out, k_token_stride, k_head_stride, k_out_token_stride, k_out_head_stride, Hk};
+    // (a tensor without heads counts as in place, whatever its pointers: the kernels' units per head depend on it)
+    p.t[0] = RopeTensor{q, Hq ? q_out : q, q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride, Hq};
+    p.t[1] = RopeTensor{k, Hk ? k_out : k, k_token_stride, k_head_stride, k_out_token_stride, k_out_head_stride, Hk};
     p.T = T;
     p.D = D;
     p.R = rotary_dim;

@@ -313,6 +313,23 @@ def test_rope_strided_and_in_place(hq, D, R, offset):
     assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(qkv[:, (Hq + Hk) * D:], rest)
 
 
+def test_rope_without_heads_on_one_side(hq):
+    """q without heads but with pointers, k in place; and the other way round."""
+    g = _gen(24)
+    T, H, D, R = 5, 3, 256, 88
+    x, pos = _normal(g, T, H, D, dtype=BF16), torch.randint(0, 9999, (T,), generator=g, device="cuda")
+    inv, _ = hq.rope_inv_freq(R)
+    other = torch.full_like(x, 7.0)
+    for layout in (hq.HQ_ROPE_HALVES, hq.HQ_ROPE_INTERLEAVED):
+        want, _ = hq.rope(x, None, pos, inv, layout=layout)
+        for heads in ((0, H), (H, 0)):
+            y = x.clone()
+            side = [(y, H * D, D, n, y) if n else (other, H * D, D, 0, x) for n in heads]
+            hq.hq_rope(hq.HQ_DT_BF16, *side[0][:4], *side[1][:4], T, D, pos, inv, R, 0, layout, 1.0, 0, side[0][4], H * D, D,
+                       side[1][4], H * D, D)
+            assert torch.equal(y, want) and bool((other == 7.0).all())
+
+
 # ------------------------------------------------------------------- slots
 def _slots_by_hand(lens, new, table, stack, count, page, n_slots):
     B, W = table.shape
