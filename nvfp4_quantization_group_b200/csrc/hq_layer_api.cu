@@ -192,8 +192,8 @@ hq_status hq_rope(int dtype, const void* q, int64_t q_token_stride, int64_t q_he
     if (!sms) return HQ_ERR_CUDA;
     RopeParams p;
     // (a tensor without heads counts as in place, whatever its pointers: the kernels' units per head depend on it)
-    p.t[0] = RopeTensor{q, Hq ? q_out : q, q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride, Hq};
-    p.t[1] = RopeTensor{k, Hk ? k_out : k, k_token_stride, k_head_stride, k_out_token_stride, k_out_head_stride, Hk};
+    p.t[0] = RopeTensor{q, Hq ? q_out : const_cast<void*>(q), q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride, Hq};
+    p.t[1] = RopeTensor{k, Hk ? k_out : const_cast<void*>(k), k_token_stride, k_head_stride, k_out_token_stride, k_out_head_stride, Hk};
     p.T = T;
     p.D = D;
     p.R = rotary_dim;
@@ -365,7 +365,7 @@ hq_status hq_kv4_attention(int dtype, const void* q, int64_t q_token_stride, int
     p.q_len = q_len;
     p.page_shift = shift;
     p.scale = scale;
-    p.window = window;
+    p.window = window < (1 << 30) ? window : 1 << 30;  // (no token is farther back: position - window stays in 32 bits)
     p.sinks = sinks;
     p.rotate = hadamard_n == 128;
     p.ws = static_cast<uint32_t*>(ws);
