@@ -652,7 +652,9 @@ hq_status hq_kv4_gather(int dtype, const uint8_t *cache, int64_t num_pages, int 
  *  A query at position p sees the tokens t <= p, and with window > 0 only those
  *  with p - t < window or t < sinks.
  *   s_t = scale * q . k_t, out = sum_t softmax(s)_t v_t, lse = ln sum_t exp s_t
- *  over the tokens it sees; none: out = 0, lse = -inf.
+ *  over the tokens it sees; none: out = 0, lse = -inf.  (Scores times log2(e)
+ *  below -1e30 count as not seen.  A query with a NaN or an infinity gets NaNs, in its
+ *  own rows only.)
  *  hadamard_n the one that the cache was written with: q is rotated before,
  *             out rotated back after (rotations keep q . k).
  *  lse_opt    float [Tq, Hq] or NULL.

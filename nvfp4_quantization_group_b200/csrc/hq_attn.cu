@@ -611,9 +611,9 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
             float a = max3(fmaxf(fabsf(y[0]), fabsf(y[1])), fabsf(y[2]), fabsf(y[3]));
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-            // 2^e in (a / 2, a]; a zero, subnormal or infinite column keeps its values
-            const uint32_t ebits = __float_as_uint(a) & 0x7F800000u;
-            const bool plain = ebits < 0x08000000u || ebits > 0x77000000u;
+            // 2^e in (a / 2, a] (at most 2^126, whose inverse is normal); a column below 2^-111 keeps its values
+            const uint32_t ebits = min(__float_as_uint(a) & 0x7F800000u, 0x7E800000u);
+            const bool plain = ebits < 0x08000000u;
             const float up = plain ? 1.0f : __uint_as_float(ebits), down = plain ? 1.0f : __uint_as_float(0x7F000000u - ebits);
             float hi[4], lo[4];
 #pragma unroll
@@ -786,7 +786,7 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
             const T h[4] = {from_f32<DT>(y[0]), from_f32<DT>(y[1]), from_f32<DT>(y[2]), from_f32<DT>(y[3])};
             *reinterpret_cast<uint2*>(out + 4 * lane) = *reinterpret_cast<const uint2*>(h);
             if (p.lse && lane == 0)
-                p.lse[row * ((int64_t)p.Hkv * p.group) + hq_] = L > 0.0f ? (mx + log2f(L)) * 0.6931471805599453f : -INFINITY;
+                p.lse[row * ((int64_t)p.Hkv * p.group) + hq_] = L != 0.0f ? (mx + log2f(L)) * 0.6931471805599453f : -INFINITY;  // (NaN stays)
         };
         // partial results: CTA c's slot 0 for a row that began before it, slot 1 for one that goes on after it
         float* const mine = parts + (size_t)(2 * blockIdx.x + (cw.ja == 0 ? 1 : 0)) * ATTN_PART;

@@ -73,6 +73,9 @@ inline bool is(const Maybe& t, const Tensor& like, at::ScalarType s) { return !t
 inline bool shaped(const Maybe& t, const Tensor& like) { return !t || t->sizes() == like.sizes(); }
 inline bool vector_of(const Tensor& t, int64_t n) { return t.dim() == 1 && t.size(0) == n; }
 inline bool rows_whole(const Maybe& t) { return !t || t->size(-1) <= 1 || t->stride(-1) == 1; }
+// Stride of dimension d, 0 where it has one entry (its stride may be anything then).
+inline int64_t step(const Tensor& t, int64_t d) { return t.size(d) > 1 ? t.stride(d) : 0; }
+inline int64_t step(const Maybe& t, int64_t d) { return t ? step(*t, d) : 0; }
 inline bool whole(const Maybe& t) { return !t || t->is_contiguous(); }
 inline Tensor make(at::IntArrayRef shape, const Tensor& like, at::ScalarType s) {
     return Tensor(at::detail::empty_cuda(shape, s, like.device(), std::nullopt));
@@ -169,11 +172,11 @@ std::tuple<Tensor, Maybe> rope(const Tensor& q, const Maybe& k, const Tensor& po
     Tensor qo = q_out ? *q_out : make({T, Hq, D}, q, q.scalar_type());
     Maybe ko = k_out;
     if (k && !ko) ko = make({T, Hk, D}, q, q.scalar_type());
-    const int s = call.rope(dt, q.data_ptr(), q.stride(0), q.stride(1), (int)Hq, ptr(k), k ? k->stride(0) : 0, k ? k->stride(1) : 0,
+    const int s = call.rope(dt, q.data_ptr(), step(q, 0), step(q, 1), (int)Hq, ptr(k), step(k, 0), step(k, 1),
                             (int)Hk, T, (int)D, static_cast<const int64_t*>(positions.data_ptr()),
                             static_cast<const double*>(inv_freq.data_ptr()), (int)(2 * inv_freq.size(0)), offset, layout,
-                            (float)magnitude, inverse, qo.data_ptr(), qo.stride(0), qo.stride(1), ptr(ko), ko ? ko->stride(0) : 0,
-                            ko ? ko->stride(1) : 0, on.stream);
+                            (float)magnitude, inverse, qo.data_ptr(), step(qo, 0), step(qo, 1), ptr(ko), step(ko, 0), step(ko, 1),
+                            on.stream);
     need(s == HQ_OK, s, what);
     return {qo, ko};
 }
@@ -221,7 +224,7 @@ void kv4_append(const Tensor& k, const Tensor& v, const Tensor& slots, const Ten
     need(rows_whole(k) && rows_whole(v) && slots.is_contiguous() && cache.is_contiguous(), HQ_ERR_ALIGN,
          "kv4_append: heads, slots and the cache have to be contiguous");
     const On on(cache);
-    const int s = call.append(dt, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
+    const int s = call.append(dt, k.data_ptr(), step(k, 0), step(k, 1), v.data_ptr(), step(v, 0), step(v, 1),
                               static_cast<const int64_t*>(slots.data_ptr()), k.size(0), (int)k.size(1), hadamard_n,
                               static_cast<uint8_t*>(cache.data_ptr()), cache.size(0), cache_page(cache), on.stream);
     need(s == HQ_OK, s, what);
@@ -273,12 +276,12 @@ std::tuple<Tensor, Maybe> kv4_attention(const Tensor& q, const Tensor& cache, co
         const int s = call.ws_init(ws->data_ptr(), ws->nbytes(), on.stream);
         need(s == HQ_OK, s, what);
     }
-    const int s = call.attention(dt, q.data_ptr(), q.stride(0), q.stride(1), Tq, (int)Hq, static_cast<const uint8_t*>(cache.data_ptr()),
+    const int s = call.attention(dt, q.data_ptr(), step(q, 0), step(q, 1), Tq, (int)Hq, static_cast<const uint8_t*>(cache.data_ptr()),
                                  cache.size(0), cache_page(cache), (int)cache.size(1), static_cast<const int32_t*>(table.data_ptr()),
                                  table.size(1), (int)lens.size(0), static_cast<const int32_t*>(lens.data_ptr()),
                                  static_cast<const int32_t*>(ptr(cu_q)), q_len,
                                  scale ? (float)*scale : 0.08838834764831845f /* 1 / sqrt(128) */, window, sinks, hadamard_n,
-                                 out.data_ptr(), out.stride(0), out.stride(1), static_cast<float*>(ptr(lse)), ws->data_ptr(),
+                                 out.data_ptr(), step(out, 0), step(out, 1), static_cast<float*>(ptr(lse)), ws->data_ptr(),
                                  ws->nbytes(), on.stream);
     need(s == HQ_OK, s, what);
     return {out, lse};
@@ -294,14 +297,18 @@ PYBIND11_MODULE(_hq_torch, m) {
             const py::object type = py::module_::import("nvfp4_quantization_group_b200").attr("HQError");
             const py::object error = type(r.status, r.what);
             PyErr_SetObject(type.ptr(), error.ptr());
+        } catch (const c10::OutOfMemoryError& e) {
+            PyErr_SetString(py::module_::import("torch").attr("OutOfMemoryError").ptr(), e.what_without_backtrace());
         }
     });
+    // (the allocator may wait for the device: other Python threads run meanwhile)
+    const py::call_guard<py::gil_scoped_release> free;
     m.def("bind", &bind);
-    m.def("add_rmsnorm", &add_rmsnorm);
-    m.def("rmsnorm_backward", &rmsnorm_backward);
-    m.def("rope", &rope);
-    m.def("kv_slots", &kv_slots);
-    m.def("kv4_append", &kv4_append);
-    m.def("kv4_gather", &kv4_gather);
-    m.def("kv4_attention", &kv4_attention);
+    m.def("add_rmsnorm", &add_rmsnorm, free);
+    m.def("rmsnorm_backward", &rmsnorm_backward, free);
+    m.def("rope", &rope, free);
+    m.def("kv_slots", &kv_slots, free);
+    m.def("kv4_append", &kv4_append, free);
+    m.def("kv4_gather", &kv4_gather, free);
+    m.def("kv4_attention", &kv4_attention, free);
 }

@@ -684,6 +684,60 @@ def test_kv4_attention_columns_do_not_touch_each_other(hq):
     assert bool(torch.isnan(out[bad]).all())
 
 
+def test_single_rows_with_any_stride(hq):
+    """A dimension of one entry has no stride to check."""
+    g = _gen(59)
+    cache, table, lens = _filled(hq, g, 1, 1, 16, [40], 128)
+    wide = [_normal(g, 1, 1, 131, dtype=BF16)[..., :128] for _ in range(3)]
+    whole = [t.contiguous() for t in wide]
+    assert wide[0].stride(0) == 131
+    c2, slot = cache.clone(), torch.tensor([7], device="cuda")
+    hq.kv4_append(wide[0], wide[1], slot, cache)
+    hq.kv4_append(whole[0], whole[1], slot, c2)
+    assert torch.equal(cache, c2)
+    assert torch.equal(hq.kv4_attention(wide[2], cache, table, lens), hq.kv4_attention(whole[2], cache, table, lens))
+
+
+def test_out_of_memory_is_the_frameworks_error(hq):
+    x = torch.zeros((1, 65536), dtype=BF16, device="cuda").expand(2 ** 31 - 1, -1)  # 2^47 bytes of codes
+    with pytest.raises(torch.OutOfMemoryError):
+        hq.add_rmsnorm_fp8_k128(x, x[0].contiguous())
+
+
+def test_kv4_attention_lse_of_nan_scores(hq):
+    g = _gen(56)
+    cache, table, lens = _filled(hq, g, 1, 1, 16, [40], 128)
+    q = _normal(g, 1, 8, 128, dtype=BF16)
+    q[0, 3, 1] = math.nan
+    _, lse = hq.kv4_attention(q, cache, table, lens, want_lse=True)
+    assert bool(torch.isnan(lse[0, 3])) and int(torch.isnan(lse).sum()) == 1
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3, 1 << 30])
+def test_kv4_attention_widest_windows(hq, window):
+    """More queries than tokens under a window as wide as the type allows: as without a window."""
+    g = _gen(57)
+    cache, table, lens = _filled(hq, g, 2, 1, 16, [2, 70], 128)
+    q = _normal(g, 10, 4, 128, dtype=BF16)
+    want = hq.kv4_attention(q, cache, table, lens, q_len=5, want_lse=True)
+    got = hq.kv4_attention(q, cache, table, lens, q_len=5, window=window, want_lse=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_kv4_attention_largest_queries(hq):
+    """Queries of 2^100 to the type's largest power of two, the scale their inverse: as the queries brought down before."""
+    g = _gen(58)
+    cache, table, lens = _filled(hq, g, 1, 1, 16, [300], 0)
+    q = _normal(g, 1, 8, 128, dtype=BF16).clamp(-1.9, 1.9)
+    want = hq.kv4_attention(q, cache, table, lens, scale=0.125, hadamard_n=0, want_lse=True)
+    for e in (100, 112, 126, 127):
+        up = q * 2.0 ** e
+        assert bool(torch.isfinite(up).all())
+        got = hq.kv4_attention(up, cache, table, lens, scale=2.0 ** (-3 - e), hadamard_n=0, want_lse=True)
+        # powers of two only; at 2^127 the column's power is one too small: FP16 parts of twice the size, the same bits
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), e
+
+
 def test_kv4_attention_extreme_scores(hq):
     """Scores of thousands: the running maximum carries them; one token takes all the weight."""
     g = _gen(52)
