@@ -15,7 +15,7 @@
 // (hi + lo, 22 bits), so scores are FP32-like.  The weights P are rounded to FP16
 // once for BF16 outputs, whose own rounding is eight times as coarse; for FP16
 // outputs they too go in two parts (the error against 64 bits is then the output's
-// own, 2.1e-4, where one part gives 2.9e-4; 118 -> 127 us at the sizes below).
+// own, 2.1e-4, where one part gives 2.9e-4; 116 -> 125 us at the sizes below).
 // The cache's byte order gives each lane its operands of a group as 16-byte
 // pieces (four for the codes, three for the block scales).  A warp takes one
 // or two groups (a unit) at a time, copied into its own ring by bulk copies that
@@ -30,10 +30,10 @@
 // Bound: the codes and scales are 152 bytes per token and key/value head, but a
 // group also costs about 390 warp instructions, 64 of them conversions of code
 // pairs at half rate.  32 requests of 8000 to 16384 tokens, 64 query and 8
-// key/value heads: 118 us, 4.0 TB/s (62 % of the measured copy rate); issue slots
+// key/value heads: 116 us, 4.1 TB/s (64 % of the measured copy rate); issue slots
 // 60 % busy, ALU 52 %, matrix 29 %; without the loads it takes about 120, without
 // the arithmetic 83.  Steps there: one group a turn 166, two 133, look-ups by
-// whole lanes 121.  (These matrix instructions, not tcgen05: that one reads its
+// whole lanes 121, both groups' scores together 116.  (These matrix instructions, not tcgen05: that one reads its
 // operands from shared memory, where K and V would have to be widened first: 512
 // bytes per token and head written and read again, 8 clocks of an SM's shared
 // memory beside the 2.4 of the codes, where the whole loop takes 10.5.)
@@ -322,6 +322,77 @@ __device__ __forceinline__ void attn_scores(const uint8_t* grp, const uint4 (*q)
         s[n][1] = __fmul_rn(s[n][1], __fmul_rn(d0, a.qs[n][1]));
         s[n][2] = __fmul_rn(s[n][2], __fmul_rn(d1, a.qs[n][0]));
         s[n][3] = __fmul_rn(s[n][3], __fmul_rn(d1, a.qs[n][1]));
+    }
+}
+
+// The same of the two groups of a unit, block by block: q is read once for both,
+// and one running product each is enough (two each: 117 us at the sizes above, the
+// groups one after the other with four: 118).
+template <int NT>
+__device__ __forceinline__ void attn_scores2(const uint8_t* unit, const uint4 (*q)[8][32], const AttnState<NT>& a, int lane,
+                                             float (&s)[2][NT][4]) {
+    const int g = lane >> 2;
+    uint32_t kw[2][2][4], sf[2][2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const uint8_t* grp = unit + h * KV_GROUP_BYTES;
+            const uint4 k = *reinterpret_cast<const uint4*>(grp + KV_K_CODES + lane * 16 + 512 * r);
+            const uint2 f = *reinterpret_cast<const uint2*>(grp + KV_K_SF + g * 8 + 64 * r);
+            kw[h][r][0] = k.x;
+            kw[h][r][1] = k.y;
+            kw[h][r][2] = k.z;
+            kw[h][r][3] = k.w;
+            e4m3x4_to_f16(f.x, sf[h][r][0], sf[h][r][1]);
+            e4m3x4_to_f16(f.y, sf[h][r][2], sf[h][r][3]);
+        }
+    float c[2][NT][4];
+#pragma unroll
+    for (int b2 = 0; b2 < 4; ++b2) {
+        uint32_t a0[2][4], a1[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            e2m1x8_to_f16(kw[h][0][b2], a0[h]);
+            e2m1x8_to_f16(kw[h][1][b2], a1[h]);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint4 f[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) f[n] = q[n][2 * b2 + k][lane];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t x0 = sf[h][0][b2], x1 = sf[h][1][b2];
+                const uint32_t m0 = k ? hmul2_half<true>(a0[h][2], x0) : hmul2_half<false>(a0[h][0], x0);
+                const uint32_t m1 = k ? hmul2_half<true>(a1[h][2], x1) : hmul2_half<false>(a1[h][0], x1);
+                const uint32_t m2 = k ? hmul2_half<true>(a0[h][3], x0) : hmul2_half<false>(a0[h][1], x0);
+                const uint32_t m3 = k ? hmul2_half<true>(a1[h][3], x1) : hmul2_half<false>(a1[h][1], x1);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (b2 == 0 && k == 0) {
+                        mma16816_first(c[h][n], m0, m1, m2, m3, f[n].x, f[n].y);
+                        mma16816(c[h][n], m0, m1, m2, m3, f[n].z, f[n].w);
+                    } else {
+                        mma16816(c[h][n], m0, m1, m2, m3, f[n].x, f[n].y);
+                        mma16816(c[h][n], m0, m1, m2, m3, f[n].z, f[n].w);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint8_t* grp = unit + h * KV_GROUP_BYTES;
+        const float d0 = *reinterpret_cast<const float*>(grp + KV_K_DEC + 4 * g);
+        const float d1 = *reinterpret_cast<const float*>(grp + KV_K_DEC + 4 * g + 32);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            s[h][n][0] = __fmul_rn(c[h][n][0], __fmul_rn(d0, a.qs[n][0]));
+            s[h][n][1] = __fmul_rn(c[h][n][1], __fmul_rn(d0, a.qs[n][1]));
+            s[h][n][2] = __fmul_rn(c[h][n][2], __fmul_rn(d1, a.qs[n][0]));
+            s[h][n][3] = __fmul_rn(c[h][n][3], __fmul_rn(d1, a.qs[n][1]));
+        }
     }
 }
 
@@ -668,10 +739,10 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                 if (ok == 3u && t0 + 31 <= pos_min && (p.window == 0 || pos_max - t0 < p.window || t0 + 31 < p.sinks)) {
                     // every column sees every token
                     float s[2][NT][4], v[2][2];
+                    attn_scores2<NT>(unit, sh.q, a, lane, s);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint8_t* grp = unit + h * KV_GROUP_BYTES;
-                        attn_scores<NT>(grp, sh.q, a, lane, s[h]);
                         v[h][0] = *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g);
                         v[h][1] = *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g + 32);
                     }
@@ -878,7 +949,7 @@ template <int DT, int NT, int W, int MINB> static int launch_t(const AttnParams&
 
 int launch_attn(int dtype, const AttnParams& p, int sms, cudaStream_t st) {
     // Two column tiles of 8 in one pass cost about 1.8 times one (16 requests of
-    // 8000 to 16000 tokens: 16 columns 60 us against 65 one by one, 32 columns 95
+    // 8000 to 16000 tokens: 16 columns 58 us against 65 one by one, 32 columns 92
     // against 114; up to 20 columns, three tiles, 43 against 37 where they leave
     // half a pass empty), so they are paired when their number is even.
     const bool wide = ((int64_t)p.q_len * p.group + 7) / 8 % 2 == 0;
