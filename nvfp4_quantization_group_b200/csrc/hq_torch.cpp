@@ -81,6 +81,15 @@ inline Tensor make(at::IntArrayRef shape, const Tensor& like, at::ScalarType s) 
     return Tensor(at::detail::empty_cuda(shape, s, like.device(), std::nullopt));
 }
 
+// `n` entries of a vector from entry `at` on, as a tensor of its own on the same memory (one allocation for the
+// small outputs of a call, whose lives are one step's: an allocation costs more than the rest of the bookkeeping).
+inline Tensor part(const Tensor& t, int64_t at, int64_t n) {
+    Tensor r = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(t.storage()), t.key_set(), t.dtype());
+    r.unsafeGetTensorImpl()->set_storage_offset(at);
+    r.unsafeGetTensorImpl()->set_sizes_contiguous(n);
+    return r;
+}
+
 // Makes the tensors' device current and gives its current stream.
 struct On {
     c10::cuda::CUDAGuard guard;
@@ -191,16 +200,17 @@ std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor, Tensor> kv_slots(const Tensor
              fits(count, lens) && fits(lens_out, lens) && fits(count_out, lens),
          HQ_ERR_UNSUPPORTED, "kv_slots: int32 tensors of one CUDA device are needed");
     need(lens.dim() == 1 && add.sizes() == lens.sizes() && table.dim() == 2 && table.size(0) == lens.size(0) && pages.dim() == 1 &&
-             count.numel() == 1 && shaped(lens_out, lens) && (!count_out || count_out->numel() == 1) && n_slots >= 0 &&
+             count.numel() == 1 && shaped(lens_out, lens) && (!count_out || count_out->numel() == 1) && n_slots >= 0 && n_slots <= INT32_MAX &&
              lens.size(0) <= INT32_MAX,
          HQ_ERR_SHAPE, "kv_slots: lens and new_tokens are [B], block_table is [B, width], free_count is [1]");
     need(lens.is_contiguous() && add.is_contiguous() && table.is_contiguous() && pages.is_contiguous() && whole(lens_out),
          HQ_ERR_ALIGN, "kv_slots: tensors have to be contiguous");
     const int64_t B = lens.size(0);
     const On on(lens);
-    Tensor lo = lens_out ? *lens_out : make({B}, lens, at::kInt), cu = make({B + 1}, lens, at::kInt);
-    Tensor slots = make({n_slots}, lens, at::kLong), positions = make({n_slots}, lens, at::kLong);
-    Tensor co = count_out ? *count_out : make({1}, lens, at::kInt), status = make({1}, lens, at::kInt);
+    const Tensor words = make({2 * B + 3}, lens, at::kInt), rows = make({2 * n_slots}, lens, at::kLong);
+    Tensor cu = part(words, 0, B + 1), status = part(words, B + 1, 1);
+    Tensor lo = lens_out ? *lens_out : part(words, B + 3, B), co = count_out ? *count_out : part(words, B + 2, 1);
+    Tensor slots = part(rows, 0, n_slots), positions = part(rows, n_slots, n_slots);
     auto i32 = [](const Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); };
     auto i64 = [](const Tensor& t) { return static_cast<int64_t*>(t.data_ptr()); };
     const int s = call.slots((int)B, i32(lens), i32(add), i32(table), table.size(1), i32(pages), pages.size(0), i32(count), page_size,
