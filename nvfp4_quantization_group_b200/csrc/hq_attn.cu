@@ -118,16 +118,6 @@ __device__ __forceinline__ int request_of(const AttnParams& p, const uint64_t* p
     }
     return lo;
 }
-// The first unit of CTA c (U for c == G).
-__device__ __forceinline__ uint64_t cta_first(const AttnParams& p, const uint64_t* pre, int nc, int us, const Sched& s,
-                                              uint32_t c) {
-    const uint64_t u = s.U * c / s.G;
-    if (c == s.G) return u;
-    const int b = request_of(p, pre, u);
-    const uint32_t n = (uint32_t)attn_request(p, b, nc, us).n, in = (uint32_t)((u - pre[b]) % n);
-    return in <= ATTN_ROW_COST ? u - in : u;
-}
-
 __device__ __forceinline__ void walk_piece(const uint64_t* pre, Walk& w) {
     w.live = w.at < w.end;
     if (!w.live) return;
@@ -138,15 +128,29 @@ __device__ __forceinline__ void walk_piece(const uint64_t* pre, Walk& w) {
     const uint64_t left = w.end - w.at;
     w.jb = left < (uint64_t)(w.r.n - w.ja) ? w.ja + (int)left : w.r.n;
 }
-__device__ __forceinline__ void walk_start(const AttnParams& p, const uint64_t* pre, int nc, int us, uint64_t at, uint64_t end,
-                                           Walk& w) {
-    w.at = at;
-    w.end = end;
-    w.live = at < end;
-    if (!w.live) return;
-    w.b = request_of(p, pre, at);
+// The first unit of CTA c (U for c == G), and where it lies (only for c < G): w.at, b, r, row, ja.
+__device__ __forceinline__ void walk_cut(const AttnParams& p, const uint64_t* pre, int nc, int us, const Sched& s, uint32_t c,
+                                         Walk& w) {
+    w.at = s.U * c / s.G;
+    if (c == s.G) return;
+    w.b = request_of(p, pre, w.at);
     w.r = attn_request(p, w.b, nc, us);
-    walk_piece(pre, w);
+    const uint64_t in = w.at - pre[w.b];
+    w.row = (int)(in / (uint32_t)w.r.n);
+    w.ja = (int)(in - (uint64_t)w.row * w.r.n);
+    if (w.ja <= ATTN_ROW_COST) {
+        w.at -= w.ja;
+        w.ja = 0;
+    }
+}
+// The rest of the piece that starts there, up to unit `end` at most.
+__device__ __forceinline__ void walk_start(Walk& w, uint64_t end) {
+    w.end = end;
+    w.live = w.at < end;
+    if (!w.live) return;
+    w.head = w.row / w.r.tiles;
+    const uint64_t left = end - w.at;
+    w.jb = left < (uint64_t)(w.r.n - w.ja) ? w.ja + (int)left : w.r.n;
 }
 __device__ __forceinline__ void walk_next(const AttnParams& p, const uint64_t* pre, int nc, int us, Walk& w) {
     w.at += (uint64_t)(w.jb - w.ja);
@@ -254,7 +258,7 @@ template <int NT, int W> struct AttnShared {
     Walk cw, nw;   // the CTA's current piece and the one after it
     Walk lw[W];    // the piece of each warp's next load
     uint64_t full[W][ATTN_STAGES];
-    unsigned long long warp_sums[W];
+    ulonglong2 warp_sums[W];
     int last;
     // then the units before each request, uint64_t [B + 1]
 };
@@ -516,38 +520,56 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
     if (lane < S) mbar_init(&sh.full[w][lane], 1);
     // ---- units before each request: units of one group while there are few
     // (latency counts), of two otherwise (fewer turns of the loops)
+    // (both are summed at once; the second pass is only for more requests than threads)
     Sched sc;
     int us = 0;
-    for (;; ++us) {
-        unsigned long long carry = 0;
+    for (bool again = true; again;) {
+        unsigned long long carry[2] = {0, 0}, mine[2] = {0, 0};
         for (int b0 = 0; b0 < p.B; b0 += 32 * W) {
             const int b = b0 + tid;
-            unsigned long long v = 0;
-            if (b < p.B) {
-                const Request r = attn_request(p, b, NC, us);
-                v = (unsigned long long)r.tiles * p.Hkv * r.n;
-            }
-            unsigned long long s = v;
+            unsigned long long v[2] = {0, 0}, s[2];
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned long long u = __shfl_up_sync(0xFFFFFFFFu, s, o);
-                if (lane >= o) s += u;
+            for (int k = 0; k < 2; ++k) {
+                if (b < p.B) {
+                    const Request r = attn_request(p, b, NC, k);
+                    v[k] = (unsigned long long)r.tiles * p.Hkv * r.n;
+                }
+                s[k] = v[k];
             }
-            if (lane == 31) sh.warp_sums[w] = s;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const unsigned long long u = __shfl_up_sync(0xFFFFFFFFu, s[k], o);
+                    if (lane >= o) s[k] += u;
+                }
+            if (lane == 31) sh.warp_sums[w] = make_ulonglong2(s[0], s[1]);
             __syncthreads();
-            unsigned long long before = carry, total = 0;
+            mine[0] = carry[0] + s[0] - v[0];
+            mine[1] = carry[1] + s[1] - v[1];
+#pragma unroll
             for (int k = 0; k < W; ++k) {
-                if (k < w) before += sh.warp_sums[k];
-                total += sh.warp_sums[k];
+                const ulonglong2 t = sh.warp_sums[k];
+                if (k < w) {
+                    mine[0] += t.x;
+                    mine[1] += t.y;
+                }
+                carry[0] += t.x;
+                carry[1] += t.y;
             }
-            if (b < p.B) pre[b] = before + s - v;
-            carry += total;
+            if (b < p.B) pre[b] = us ? mine[1] : mine[0];
             __syncthreads();
         }
-        if (tid == 0) pre[p.B] = carry;
-        sc.U = carry;
-        if (us == 1 || carry <= 2ull * W * gridDim.x) break;
+        sc.U = us ? carry[1] : carry[0];
+        again = false;
+        if (us == 0 && sc.U > 2ull * W * gridDim.x) {
+            us = 1;
+            sc.U = carry[1];
+            again = p.B > 32 * W;
+            if (!again && tid < p.B) pre[tid] = mine[1];
+        }
     }
+    if (tid == 0) pre[p.B] = sc.U;
     fence_mbar_init();
     __syncthreads();
     if (blockIdx.x == 0)
@@ -571,9 +593,9 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
     Walk& lw = sh.lw[w];
     {
         // (lanes 0 and 1 find the two ends side by side)
-        const uint64_t end = cta_first(p, pre, NC, us, sc, blockIdx.x + (lane & 1));
         Walk t;
-        walk_start(p, pre, NC, us, __shfl_sync(0xFFFFFFFFu, end, 0), __shfl_sync(0xFFFFFFFFu, end, 1), t);
+        walk_cut(p, pre, NC, us, sc, blockIdx.x + (lane & 1), t);
+        walk_start(t, __shfl_sync(0xFFFFFFFFu, t.at, 1));  // (lane 0's is the CTA's)
         if (tid == 0) cw = t;
         if (lane == 0) lw = t;
     }
