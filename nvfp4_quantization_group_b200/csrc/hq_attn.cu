@@ -223,6 +223,12 @@ __device__ __forceinline__ void mbar_arrive_expect(uint64_t* bar, uint32_t bytes
                  :: "r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
+__device__ __forceinline__ uint32_t arrive(uint32_t* p) {
+    uint32_t r;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(r) : "l"(p) : "memory");
+    return r;
+}
+
 // 128-point butterfly over a warp, lane l with elements 4 l .. 4 l + 3, and
 // the factor 1 / sqrt(128).
 __device__ __forceinline__ void rotate_warp(float (&y)[4], int lane) {
@@ -907,16 +913,15 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
         if (!complete) {
             // the CTA that arrives last joins the row's partial results, in the order of its CTAs
             const uint32_t first = cta_of(sc, u0 + ATTN_ROW_COST), last = cta_of(sc, u0 + cw.r.n - 1);
-            __threadfence();
+            // (one thread releases what all wrote before the barrier, and acquires for all after the next one)
             __syncthreads();
             if (tid == 0) {
-                const uint32_t seen = atomicAdd(p.ws + 64 + first, 1u);
+                const uint32_t seen = arrive(p.ws + 64 + first);
                 sh.last = seen == last - first;
                 if (sh.last) p.ws[64 + first] = 0;  // rest state
             }
             __syncthreads();
             if (sh.last) {
-                __threadfence();
                 for (int c = w; c < tile_cols; c += W) {
                     float mx = ATTN_NONE, L = 0.0f, y[4] = {};
                     for (uint32_t k0 = first; k0 <= last; k0 += 4) {  // four results on their way at a time
