@@ -15,7 +15,7 @@
 // (hi + lo, 22 bits), so scores are FP32-like.  The weights P are rounded to FP16
 // once for BF16 outputs, whose own rounding is eight times as coarse; for FP16
 // outputs they too go in two parts (the error against 64 bits is then the output's
-// own, 2.1e-4, where one part gives 2.9e-4; 116 -> 125 us at the sizes below).
+// own, 2.1e-4, where one part gives 2.9e-4; 114 -> 123 us at the sizes below).
 // The cache's byte order gives each lane its operands of a group as 16-byte
 // pieces (four for the codes, three for the block scales).  A warp takes one
 // or two groups (a unit) at a time, copied into its own ring by bulk copies that
@@ -28,24 +28,27 @@
 // largest seen so far, at or below 1.
 //
 // Bound: the codes and scales are 152 bytes per token and key/value head, but a
-// group also costs about 390 warp instructions, 64 of them conversions of code
+// group also costs about 370 warp instructions, 64 of them conversions of code
 // pairs at half rate.  32 requests of 8000 to 16384 tokens, 64 query and 8
-// key/value heads: 116 us, 4.1 TB/s (64 % of the measured copy rate); issue slots
-// 60 % busy, ALU 52 %, matrix 29 %; without the loads it takes about 120, without
-// the arithmetic 83.  Steps there: one group a turn 166, two 133, look-ups by
-// whole lanes 121, both groups' scores together 116.  (These matrix instructions, not tcgen05: that one reads its
-// operands from shared memory, where K and V would have to be widened first: 512
-// bytes per token and head written and read again, 8 clocks of an SM's shared
-// memory beside the 2.4 of the codes, where the whole loop takes 10.5.)
+// key/value heads: 114 us, 4.2 TB/s (64 % of the measured copy rate); issue slots
+// 59 % busy, ALU 53 %, matrix 31 %, no more than four warps a scheduler to fill the
+// gaps (128 registers each; 96 would spill).  Steps there: one group a turn 166,
+// two 133, look-ups by whole lanes 121, both groups' scores together 116.  (These
+// matrix instructions, not tcgen05: that one reads its operands from shared memory,
+// where K and V would have to be widened first: 512 bytes per token and head
+// written and read again, 8 clocks of an SM's shared memory beside the 2.4 of the
+// codes, where the whole loop takes 10.)
 #include "hq_layer.cuh"
 
 namespace hq {
 
 constexpr int ATTN_STAGES = 2;       // units in flight per warp
-// Units that a row's start and end (its q, the joins) are worth: 48 requests
-// with a window of 2047 tokens and up to 20 columns take 47 us with 8, 40 with
-// 12, 37 with 16 or 24.
-constexpr int ATTN_ROW_COST = 16;
+// Units that a row's start and end (its q, the joins) are worth.  48 requests with
+// a window of 2047 tokens and up to 20 columns take 39.4 us with 10, 36.6 with 16,
+// 36.0 with 24, 35.5 with 28; 16 requests of 12000 tokens 41.1, 39.5, 38.2, 38.3; a
+// batch of 4 short requests 10.8, 10.7, 11.0, 11.0 (a cost that goes by the units'
+// size takes a register too many: 115 us instead of 114 for the largest batch).
+constexpr int ATTN_ROW_COST = 24;
 constexpr int ATTN_MAX_CTAS = 512;   // workspace: CTAs of a launch at most
 constexpr int ATTN_MAX_NC = 16;
 constexpr int ATTN_PART = ATTN_MAX_NC * (128 + 2);  // floats of one partial result
@@ -977,7 +980,7 @@ template <int DT, int NT, int W, int MINB> static int launch_t(const AttnParams&
 int launch_attn(int dtype, const AttnParams& p, int sms, cudaStream_t st) {
     // Two column tiles of 8 in one pass cost about 1.8 times one (16 requests of
     // 8000 to 16000 tokens: 16 columns 58 us against 65 one by one, 32 columns 92
-    // against 114; up to 20 columns, three tiles, 43 against 37 where they leave
+    // against 114; up to 20 columns, three tiles, 44 against 38 where they leave
     // half a pass empty), so they are paired when their number is even.
     const bool wide = ((int64_t)p.q_len * p.group + 7) / 8 % 2 == 0;
     if (dtype == HQ_DT_BF16)
