@@ -925,35 +925,45 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
             }
             __syncthreads();
             if (sh.last) {
-                for (int c = w; c < tile_cols; c += W) {
-                    float mx = ATTN_NONE, L = 0.0f, y[4] = {};
-                    for (uint32_t k0 = first; k0 <= last; k0 += 4) {  // four results on their way at a time
-                        float2 ml[4];
-                        float4 v[4];
+                float mx[CPW], L[CPW], y[CPW][4];
+#pragma unroll
+                for (int x = 0; x < CPW; ++x) {
+                    mx[x] = ATTN_NONE;
+                    L[x] = y[x][0] = y[x][1] = y[x][2] = y[x][3] = 0.0f;
+                }
+                for (uint32_t k0 = first; k0 <= last; k0 += 4) {  // four results of the warp's columns on their way at a time
+                    float2 ml[CPW][4];
+                    float4 v[CPW][4];
+#pragma unroll
+                    for (int x = 0; x < CPW; ++x)
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
                             const uint32_t k = k0 + z;
+                            const int c = w + x * W;
                             const float* part = parts + (size_t)(2 * k + (k == first ? 1 : 0)) * ATTN_PART;
-                            ml[z] = make_float2(ATTN_NONE, 0.0f);
-                            v[z] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            if (k <= last) {
-                                ml[z] = __ldcg(reinterpret_cast<const float2*>(part + ATTN_MAX_NC * 128 + 2 * c));
-                                v[z] = __ldcg(reinterpret_cast<const float4*>(part + c * 128 + 4 * lane));
+                            ml[x][z] = make_float2(ATTN_NONE, 0.0f);
+                            v[x][z] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (k <= last && c < tile_cols) {
+                                ml[x][z] = __ldcg(reinterpret_cast<const float2*>(part + ATTN_MAX_NC * 128 + 2 * c));
+                                v[x][z] = __ldcg(reinterpret_cast<const float4*>(part + c * 128 + 4 * lane));
                             }
                         }
 #pragma unroll
+                    for (int x = 0; x < CPW; ++x)
+#pragma unroll
                         for (int z = 0; z < 4; ++z) {
-                            const float t = fmaxf(mx, ml[z].x), fa = ex2(mx - t), fb = ex2(ml[z].x - t);
-                            mx = t;
-                            L = L * fa + ml[z].y * fb;
-                            y[0] = y[0] * fa + v[z].x * fb;
-                            y[1] = y[1] * fa + v[z].y * fb;
-                            y[2] = y[2] * fa + v[z].z * fb;
-                            y[3] = y[3] * fa + v[z].w * fb;
+                            const float t = fmaxf(mx[x], ml[x][z].x), fa = ex2(mx[x] - t), fb = ex2(ml[x][z].x - t);
+                            mx[x] = t;
+                            L[x] = L[x] * fa + ml[x][z].y * fb;
+                            y[x][0] = y[x][0] * fa + v[x][z].x * fb;
+                            y[x][1] = y[x][1] * fa + v[x][z].y * fb;
+                            y[x][2] = y[x][2] * fa + v[x][z].z * fb;
+                            y[x][3] = y[x][3] * fa + v[x][z].w * fb;
                         }
-                    }
-                    store(c, y, mx, L);
                 }
+#pragma unroll
+                for (int x = 0; x < CPW; ++x)
+                    if (w + x * W < tile_cols) store(w + x * W, y[x], mx[x], L[x]);
             }
         }
         __syncthreads();  // the merge buffer, q and the piece's record are free again
@@ -978,14 +988,17 @@ template <int DT, int NT, int W, int MINB> static int launch_t(const AttnParams&
 }
 
 int launch_attn(int dtype, const AttnParams& p, int sms, cudaStream_t st) {
-    // Two column tiles of 8 in one pass cost about 1.8 times one (16 requests of
-    // 8000 to 16000 tokens: 16 columns 58 us against 65 one by one, 32 columns 92
-    // against 114; up to 20 columns, three tiles, 44 against 38 where they leave
-    // half a pass empty), so they are paired when their number is even.
+    // Two column tiles of 8 in one pass cost about 1.7 times one (64 requests of
+    // 12000 tokens, 4 key/value heads: 165 us against 211 one by one; a prefill's
+    // chunks of up to 128 tokens 149 against 187; a batch of 4 short requests 16
+    // against 12), so they are paired when their number is even.  (Up to 20
+    // columns, three tiles, of 48 verifying requests: 44 us paired, half a pass
+    // empty, against 38.)  Six warps a block, as one of eight with 255 registers
+    // or two blocks of four take 172 and 167 us there.
     const bool wide = ((int64_t)p.q_len * p.group + 7) / 8 % 2 == 0;
     if (dtype == HQ_DT_BF16)
-        return wide ? launch_t<HQ_DT_BF16, 2, 4, 2>(p, sms, st) : launch_t<HQ_DT_BF16, 1, 8, 2>(p, sms, st);
-    return wide ? launch_t<HQ_DT_F16, 2, 4, 2>(p, sms, st) : launch_t<HQ_DT_F16, 1, 8, 2>(p, sms, st);
+        return wide ? launch_t<HQ_DT_BF16, 2, 6, 2>(p, sms, st) : launch_t<HQ_DT_BF16, 1, 8, 2>(p, sms, st);
+    return wide ? launch_t<HQ_DT_F16, 2, 6, 2>(p, sms, st) : launch_t<HQ_DT_F16, 1, 8, 2>(p, sms, st);
 }
 
 }  // namespace hq
