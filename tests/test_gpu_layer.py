@@ -841,14 +841,15 @@ def test_calls_on_another_stream(hq):
 
 
 # ------------------------------------------------------- sizes and neighbours
-def test_kv4_attention_of_many_requests(hq):
+@pytest.mark.parametrize("heads", [4, 16])
+def test_kv4_attention_of_many_requests(hq, heads):
     """More requests than a block has threads, most of them tiny, some empty."""
     g = _gen(81)
     B, page = 3001, 16
     lens = torch.randint(0, 40, (B,), generator=torch.Generator().manual_seed(5)).tolist()
     lens[1234] = 2000
     cache, table, t_lens = _filled(hq, g, B, 1, page, lens, 128)
-    q = _normal(g, B, 4, 128, dtype=BF16)
+    q = _normal(g, B, heads, 128, dtype=BF16)
     out, lse = hq.kv4_attention(q, cache, table, t_lens, want_lse=True)
     for b in list(range(0, B, 211)) + [1233, 1234, 1235, B - 1]:
         rows = [(0, 0)] * b + [(b, b + 1)] + [(0, 0)] * (B - b - 1)
