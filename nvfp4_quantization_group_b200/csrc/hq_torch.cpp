@@ -81,12 +81,12 @@ inline Tensor make(at::IntArrayRef shape, const Tensor& like, at::ScalarType s) 
     return Tensor(at::detail::empty_cuda(shape, s, like.device(), std::nullopt));
 }
 
-// `n` entries of a vector from entry `at` on, as a tensor of its own on the same memory (one allocation for the
-// small outputs of a call, whose lives are one step's: an allocation costs more than the rest of the bookkeeping).
-inline Tensor part(const Tensor& t, int64_t at, int64_t n) {
+// A vector's entries from `at` on, as a tensor of its own on the same memory (one allocation for the small outputs
+// of a call: an allocation costs more than the rest of the bookkeeping).
+inline Tensor part(const Tensor& t, int64_t at, at::IntArrayRef shape) {
     Tensor r = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(t.storage()), t.key_set(), t.dtype());
     r.unsafeGetTensorImpl()->set_storage_offset(at);
-    r.unsafeGetTensorImpl()->set_sizes_contiguous(n);
+    r.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
     return r;
 }
 
@@ -117,12 +117,14 @@ std::tuple<Tensor, Tensor, Maybe, Maybe, Maybe> add_rmsnorm(const Tensor& x, con
     Tensor codes = make({M, K}, x, at::kByte);
     const bool transposed = (layout & ~HQ_FP8_UE8M0) == HQ_SCALE_TRANSPOSED;
     const int64_t ld = transposed ? scale_ld.value_or(M) : groups;
-    need(ld >= 0, HQ_ERR_SHAPE, "add_rmsnorm_fp8_k128: scale_ld");
-    Tensor scales = transposed ? make({groups, ld}, x, at::kFloat) : make({M, groups}, x, at::kFloat);
+    need(ld >= 0 && ld <= INT32_MAX, HQ_ERR_SHAPE, "add_rmsnorm_fp8_k128: scale_ld");
+    const int64_t rows = transposed ? groups : M, n = rows * ld;  // of scales; amax and rstd lie behind them
+    const Tensor floats = make({n * (want_amax ? 2 : 1) + (want_rstd ? M : 0)}, x, at::kFloat);
+    Tensor scales = part(floats, 0, {rows, ld});
     Maybe h, rstd, amax;
     if (residual) h = residual_out ? *residual_out : make({M, K}, x, x.scalar_type());
-    if (want_rstd) rstd = make({M}, x, at::kFloat);
-    if (want_amax) amax = make(scales.sizes(), x, at::kFloat);
+    if (want_amax) amax = part(floats, n, {rows, ld});
+    if (want_rstd) rstd = part(floats, n * (want_amax ? 2 : 1), {M});
     const int s = call.norm(dt, x.data_ptr(), M > 1 ? x.stride(0) : K, ptr(residual), residual && M > 1 ? residual->stride(0) : K,
                             weight.data_ptr(), wt, (float)eps, M, K, ptr(h), static_cast<uint8_t*>(codes.data_ptr()),
                             static_cast<float*>(scales.data_ptr()), layout, ld, static_cast<float*>(ptr(rstd)),
@@ -208,9 +210,9 @@ std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor, Tensor> kv_slots(const Tensor
     const int64_t B = lens.size(0);
     const On on(lens);
     const Tensor words = make({2 * B + 3}, lens, at::kInt), rows = make({2 * n_slots}, lens, at::kLong);
-    Tensor cu = part(words, 0, B + 1), status = part(words, B + 1, 1);
-    Tensor lo = lens_out ? *lens_out : part(words, B + 3, B), co = count_out ? *count_out : part(words, B + 2, 1);
-    Tensor slots = part(rows, 0, n_slots), positions = part(rows, n_slots, n_slots);
+    Tensor cu = part(words, 0, {B + 1}), status = part(words, B + 1, {1});
+    Tensor lo = lens_out ? *lens_out : part(words, B + 3, {B}), co = count_out ? *count_out : part(words, B + 2, {1});
+    Tensor slots = part(rows, 0, {n_slots}), positions = part(rows, n_slots, {n_slots});
     auto i32 = [](const Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); };
     auto i64 = [](const Tensor& t) { return static_cast<int64_t*>(t.data_ptr()); };
     const int s = call.slots((int)B, i32(lens), i32(add), i32(table), table.size(1), i32(pages), pages.size(0), i32(count), page_size,
