@@ -67,7 +67,7 @@ def _on(stream, tensors, call):
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device)
     with torch.cuda.device(device), torch.cuda.stream(s):
         for t in tensors:
-            if t is not None:
+            if t is not None and t.is_cuda:
                 t.record_stream(s)
         return call()
 

@@ -704,6 +704,13 @@ def test_out_of_memory_is_the_frameworks_error(hq):
         hq.add_rmsnorm_fp8_k128(x, x[0].contiguous())
 
 
+def test_a_tensor_on_the_host_is_refused_on_a_stream_too(hq):
+    x, w = torch.zeros((2, 128), dtype=BF16, device="cuda"), torch.zeros(128, dtype=BF16)
+    for kw in ({}, {"stream": torch.cuda.Stream()}):
+        with pytest.raises(hq.HQError):
+            hq.add_rmsnorm_fp8_k128(x, w, **kw)
+
+
 def test_kv4_attention_lse_of_nan_scores(hq):
     g = _gen(56)
     cache, table, lens = _filled(hq, g, 1, 1, 16, [40], 128)
