@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(T, MINB) add_rmsnorm_fp8_kernel(NormParams p) 
         }
         if constexpr (AHEAD) load(m + step);
         sum = WARP ? warp_sum(sum) : block_sum(sum, red[k]);
-        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fmaf_rn(sum, inv_k, p.eps)));
+        const float rstd = __frsqrt_rn(__fmaf_rn(sum, inv_k, p.eps));
         if (p.rstd && i == 0) p.rstd[m] = rstd;
 #pragma unroll
         for (int j = 0; j < J; ++j) {

@@ -14,13 +14,15 @@ constexpr int ROPE_THREADS = 256;
 
 // cos and sin of position * inv_freq, the angle reduced to turns in FP64: the
 // product keeps 53 bits, so its distance to the nearest whole turn is good to
-// |turns| 2^-52, and only that distance is rounded to FP32.
+// |turns| 2^-52.  That distance is rounded to FP32 (t), and the rest of it (d, in
+// radians, below 2 pi 2^-26) put right to first order: cos - d sin, sin + d cos.
 __device__ __forceinline__ float2 rope_cos_sin(int64_t pos, double inv_freq, float magnitude, bool inverse) {
-    const double turns = (double)pos * (inv_freq * 0.15915494309189533577);
-    const float t = (float)(turns - rint(turns));
+    const double turns = (double)pos * (inv_freq * 0.15915494309189533577), part = turns - rint(turns);
+    const float t = (float)part, d = (float)(part - (double)t) * 6.2831853f;
     float s, c;
     sincospif(2.0f * t, &s, &c);
-    return make_float2(__fmul_rn(c, magnitude), __fmul_rn(inverse ? -s : s, magnitude));
+    const float c2 = __fmaf_rn(-d, s, c), s2 = __fmaf_rn(d, c, s);
+    return make_float2(__fmul_rn(c2, magnitude), __fmul_rn(inverse ? -s2 : s2, magnitude));
 }
 
 __device__ __forceinline__ void rope_turn(float& u, float& v, float2 r) {
