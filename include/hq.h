@@ -667,9 +667,13 @@ hq_status hq_kv4_gather(int dtype, const uint8_t *cache, int64_t num_pages, int 
  * page_size tokens (tokens without a page count as not seen), to HQ_ERR_SHAPE by a
  * request whose rows reach outside [0, Tq) or are more than q_len (those left out
  * are not written).
- * Arithmetic: scores in FP32 from FP16 keys (exact) and a two-part FP16 query,
- * weights rounded to FP16 (BF16 outputs) or in two FP16 parts (FP16 outputs) for
- * the second product, sums in FP32.  Results do not
+ * Arithmetic: scores in FP32 from FP16 keys (exact) and a query in two FP16 parts
+ * (22 bits of an element, 2^-24 of its column's largest where that is more).  What
+ * a token adds, its weight times its value's decode scale, is rounded to FP16 (BF16
+ * outputs) or held in two FP16 parts (FP16 outputs) for the second product: 2^-11 or
+ * 2^-22 of it, or 2^-34 of the largest such product among the tokens that the query
+ * sees where that is more, whatever the sizes of the values.  Weights below 2^-125
+ * of the row's largest may count as zero.  Sums in FP32.  Results do not
  * depend on anything but the inputs and the GPU's SM count.
  * Alignment: q, out, cache, ws 16 bytes, strides of q and out multiples of 8.
  * Errors: HQ_ERR_NULL, HQ_ERR_SHAPE (B > HQ_KV_MAX_REQUESTS, Hq not a multiple

@@ -24,8 +24,12 @@
 //
 // The running maximum moves only when a score exceeds it by 5 (in powers of
 // two), so the usual group needs no exchange between lanes: weights stay at
-// or below 32, and the decode scales of V, folded into them relative to the
-// largest seen so far, at or below 1.
+// or below 32.  The decode scales of V are folded into them: what goes into FP16
+// is c = weight * decode scale, times a power of two per column that follows the
+// largest c of the tokens that the column sees (as the maximum does, 2^9 to 2^15),
+// never a token's scale alone: a large value without weight, outside the window, or
+// a vector of zeros (its decode scale is 1) leaves the others their bits.  A c is
+// good to 2^-11 down to 2^-23 of that largest one, to 2^-34 of it below.
 //
 // Bound: the codes and scales are 152 bytes per token and key/value head, but a
 // group also costs about 370 warp instructions, 64 of them conversions of code
@@ -51,7 +55,7 @@ constexpr int ATTN_STAGES = 2;       // units in flight per warp
 constexpr int ATTN_ROW_COST = 24;
 constexpr int ATTN_MAX_CTAS = 512;   // workspace: CTAs of a launch at most
 constexpr int ATTN_MAX_NC = 16;
-constexpr int ATTN_PART = ATTN_MAX_NC * (128 + 2);  // floats of one partial result
+constexpr int ATTN_PART = ATTN_MAX_NC * (128 + 4);  // floats of one partial result: sums, {maximum, sum, power of two}
 constexpr float ATTN_NONE = -1e30f;  // running maximum before any token
 
 // ---------------------------------------------------------------- schedule
@@ -261,7 +265,7 @@ template <int NT, int W> struct AttnShared {
         float4 frag[W / 2][NT * 8][32];   // accumulators of the upper half's warps
         float o[W / 2][NC][OS];           // results of the lower half's warps
     };
-    float m[W][NC], l[W][NC];
+    float m[W][NC], l[W][NC], z[W][NC];
     float qs[NC];  // factor of a column's scores, in powers of two
     int pos[NC];   // a column's position
     Walk cw, nw;   // the CTA's current piece and the one after it
@@ -275,10 +279,13 @@ template <int NT, int W> struct AttnShared {
 // What a lane carries through a row.
 template <int NT> struct AttnState {
     float o[NT][8][4];  // O^T: block b, rows d = 16 b + 2 g (0, 1) and + 1 (2, 3), columns 2 i, 2 i + 1
-    float m[NT][2], l[NT][2];
-    float vmax, vinv;  // largest decode scale of V so far (the accumulators are relative to it), and its inverse
+    float m[NT][2], l[NT][2];  // m: an integer, so that what moves with it are powers of two
+    float cz[NT][2];           // power of two that the second product's weights carry
     float qs[NT][2];
 };
+constexpr float ATTN_CZ_MOST = 8.507059173023462e37f;  // 2^126, before any contribution
+__device__ __forceinline__ int pow2_of(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }  // x: normal, > 0
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // e: -126 .. 127
 
 // Scores (in powers of two) of the group at `grp`: rows g, g + 8, columns 2 i,
 // 2 i + 1.
@@ -409,13 +416,11 @@ __device__ __forceinline__ void attn_scores2(const uint8_t* unit, const uint4 (*
     }
 }
 
-// Moves the references to scores s (N groups' worth) and value scales v.
+// Moves the running maxima to scores s (N groups' worth).  The accumulators stay:
+// what their weights shrink by goes to the columns' powers of two.
 template <int NT, int N>
-__device__ __forceinline__ void attn_grow(AttnState<NT>& a, const float (&s)[N][NT][4], const float (&v)[N][2]) {
-    float x = a.vmax;
-#pragma unroll
-    for (int h = 0; h < N; ++h) x = max3(x, v[h][0], v[h][1]);
-    bool grow = x > a.vmax;
+__device__ __forceinline__ void attn_grow(AttnState<NT>& a, const float (&s)[N][NT][4]) {
+    bool grow = false;
     float top[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -428,40 +433,95 @@ __device__ __forceinline__ void attn_grow(AttnState<NT>& a, const float (&s)[N][
         }
     if (!__any_sync(0xFFFFFFFFu, grow)) return;
 #pragma unroll
-    for (int k = 4; k <= 16; k <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, k));
-    const float beta = x > 0.0f ? __fdividef(a.vmax, x) : 0.0f;
-    a.vmax = x;
-    a.vinv = x > 0.0f ? __frcp_rn(x) : 0.0f;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        float f[2];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            float t = fmaxf(a.m[n][k], top[n][k]);
+            float t = top[n][k];
 #pragma unroll
             for (int y = 4; y <= 16; y <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, y));
-            f[k] = ex2(a.m[n][k] - t);
+            t = fmaxf(a.m[n][k], ceilf(t));
+            const float d = a.m[n][k] - t;
             a.m[n][k] = t;
-            a.l[n][k] *= f[k];
-            f[k] *= beta;
-        }
+            a.l[n][k] *= ex2(d);
+            // 2^-d more, as far as the range goes; the rest falls to the accumulators
+            const float e = (float)pow2_of(a.cz[n][k]) - d, z = fminf(e, 126.0f), f = ex2(z - e);
+            a.cz[n][k] = pow2((int)z);
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-            a.o[n][b][0] *= f[0];
-            a.o[n][b][1] *= f[1];
-            a.o[n][b][2] *= f[0];
-            a.o[n][b][3] *= f[1];
+            for (int b = 0; b < 8; ++b) {
+                a.o[n][b][k] *= f;
+                a.o[n][b][2 + k] *= f;
+            }
         }
-    }
 }
 
-// Adds the group's weighted values.  v: decode scales of rows g, g + 8; keep0,
-// keep1: the bytes to keep of the block scales of the lane's tokens 2 i, 2 i + 1
-// and 2 i + 8, + 9.
+// Scores s of N groups (the first at `grp`) become contributions, weight times
+// decode scale v (of rows g, g + 8), and the weights are summed.  The columns'
+// powers of two move down where a contribution would leave FP16's range, to
+// 2^9 .. 2^10 for the largest one.
+template <int NT, int N>
+__device__ __forceinline__ void attn_weigh(AttnState<NT>& a, float (&s)[N][NT][4], const float (&v)[N][2], const uint8_t* grp,
+                                           int lane) {
+    bool big = false;
+    float top[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int h = 0; h < N; ++h) {
+            const float e0 = ex2(s[h][n][0] - a.m[n][0]), e1 = ex2(s[h][n][1] - a.m[n][1]);
+            const float e2 = ex2(s[h][n][2] - a.m[n][0]), e3 = ex2(s[h][n][3] - a.m[n][1]);
+            a.l[n][0] += e0 + e2;
+            a.l[n][1] += e1 + e3;
+            s[h][n][0] = e0 * v[h][0];
+            s[h][n][1] = e1 * v[h][0];
+            s[h][n][2] = e2 * v[h][1];
+            s[h][n][3] = e3 * v[h][1];
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            top[n][k] = fmaxf(s[0][n][k], s[0][n][2 + k]);
+#pragma unroll
+            for (int h = 1; h < N; ++h) top[n][k] = max3(top[n][k], s[h][n][k], s[h][n][2 + k]);
+            big |= top[n][k] * a.cz[n][k] > 32768.0f;
+        }
+    }
+    if (!__any_sync(0xFFFFFFFFu, big)) return;
+    // vectors of zeros contribute nothing: all eight block scales of the token are zero
+    const int g = lane >> 2;
+#pragma unroll
+    for (int h = 0; h < N; ++h)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const uint4 f = *reinterpret_cast<const uint4*>(grp + h * KV_GROUP_BYTES + KV_V_SF + 64 * r + 16 * (g >> 1));
+            if (((f.x | f.y | f.z | f.w) & 0x00FF00FFu << 8 * (g & 1)) == 0)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s[h][n][2 * r] = s[h][n][2 * r + 1] = 0.0f;
+        }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float t = fmaxf(s[0][n][k], s[0][n][2 + k]);
+#pragma unroll
+            for (int h = 1; h < N; ++h) t = max3(t, s[h][n][k], s[h][n][2 + k]);
+#pragma unroll
+            for (int y = 4; y <= 16; y <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, y));
+            const int e = pow2_of(a.cz[n][k]), z = min(e, 9 - pow2_of(t));  // (weights are at most 2^5, decode scales below 2^117)
+            const float f = ex2((float)(z - e));
+            a.cz[n][k] = pow2(z);
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                a.o[n][b][k] *= f;
+                a.o[n][b][2 + k] *= f;
+            }
+        }
+}
+
+// Adds the group's weighted values.  s: contributions (attn_weigh); keep0, keep1:
+// the bytes to keep of the block scales of the lane's tokens 2 i, 2 i + 1 and
+// 2 i + 8, + 9.
 template <int NT, bool MASK, bool FINE>
 __device__ __forceinline__ void attn_values(const uint8_t* grp, AttnState<NT>& a, const float (&s)[NT][4],
-                                            const float (&v)[2], uint32_t keep0, uint32_t keep1, int lane) {
-    const float r0 = v[0] * a.vinv, r1 = v[1] * a.vinv;
+                                            uint32_t keep0, uint32_t keep1, int lane) {
     uint4 vf0 = *reinterpret_cast<const uint4*>(grp + KV_V_SF + (lane & 3) * 16);
     uint4 vf1 = *reinterpret_cast<const uint4*>(grp + KV_V_SF + (lane & 3) * 16 + 64);
     if constexpr (MASK) {
@@ -471,11 +531,8 @@ __device__ __forceinline__ void attn_values(const uint8_t* grp, AttnState<NT>& a
     uint32_t pb[NT][2], pl[NT][2];  // weights as the n side: column g, tokens 2 i, 2 i + 1 and 2 i + 8, + 9; FINE: their rest
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const float e0 = ex2(s[n][0] - a.m[n][0]), e1 = ex2(s[n][1] - a.m[n][1]);
-        const float e2 = ex2(s[n][2] - a.m[n][0]), e3 = ex2(s[n][3] - a.m[n][1]);
-        a.l[n][0] += e0 + e2;
-        a.l[n][1] += e1 + e3;
-        const float w0 = e0 * r0, w1 = e1 * r0, w2 = e2 * r1, w3 = e3 * r1;
+        const float w0 = s[n][0] * a.cz[n][0], w1 = s[n][1] * a.cz[n][1];
+        const float w2 = s[n][2] * a.cz[n][0], w3 = s[n][3] * a.cz[n][1];
         const uint32_t u = pack_h2(w0, w1), v2 = pack_h2(w2, w3);
         pb[n][0] = transpose8x8(u);
         pb[n][1] = transpose8x8(v2);
@@ -747,13 +804,13 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                 a.qs[n][k] = sh.qs[c];
                 a.m[n][k] = ATTN_NONE;
                 a.l[n][k] = 0.0f;
+                a.cz[n][k] = ATTN_CZ_MOST;
             }
 #pragma unroll
             for (int b = 0; b < 8; ++b)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) a.o[n][b][e] = 0.0f;
         }
-        a.vmax = a.vinv = 0.0f;
 
         for (int j = own(cw) + w; j < cw.jb; j += W) {
             const int cur = st;
@@ -777,9 +834,10 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                         v[h][0] = *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g);
                         v[h][1] = *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g + 32);
                     }
-                    attn_grow<NT, 2>(a, s, v);
+                    attn_grow<NT, 2>(a, s);
+                    attn_weigh<NT, 2>(a, s, v, unit, lane);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) attn_values<NT, false, FINE>(unit + h * KV_GROUP_BYTES, a, s[h], v[h], 0u, 0u, lane);
+                    for (int h = 0; h < 2; ++h) attn_values<NT, false, FINE>(unit + h * KV_GROUP_BYTES, a, s[h], 0u, 0u, lane);
                 } else if (t0 <= pos_max && !(p.window > 0 && t0 + 31 <= pos_min - p.window && t0 >= p.sinks)) {
                     // some do (in a chunk of a prefill, a unit may be ahead of all of these columns, or behind their window)
 #pragma unroll 1
@@ -803,8 +861,9 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                         const int e = pos_max - t1 - 2 * i4;  // the lane's even token is real if e >= 0, the odd one if e >= 1
                         const uint32_t keep0 = (e >= 0 ? 0x00FF00FFu : 0u) | (e >= 1 ? 0xFF00FF00u : 0u);
                         const uint32_t keep1 = (e >= 8 ? 0x00FF00FFu : 0u) | (e >= 9 ? 0xFF00FF00u : 0u);
-                        attn_grow<NT, 1>(a, s, v);
-                        attn_values<NT, true, FINE>(grp, a, s[0], v[0], keep0, keep1, lane);
+                        attn_grow<NT, 1>(a, s);
+                        attn_weigh<NT, 1>(a, s, v, grp, lane);
+                        attn_values<NT, true, FINE>(grp, a, s[0], keep0, keep1, lane);
                     }
                 }
             }
@@ -823,20 +882,23 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                 if (g == 0) {
                     sh.m[w][8 * n + 2 * i4 + k] = a.m[n][k];
                     sh.l[w][8 * n + 2 * i4 + k] = t;
+                    sh.z[w][8 * n + 2 * i4 + k] = (float)-pow2_of(a.cz[n][k]);
                 }
             }
         __syncthreads();
         if (sh.nw.live) load_q(sh.nw);
-        float M[NT][2];
+        // a warp's accumulators are relative to 2^(m + z); in common: the largest of these
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int c = 8 * n + 2 * i4 + k;
-                M[n][k] = ATTN_NONE;
+                float M = ATTN_NONE, Z = ATTN_NONE;
 #pragma unroll
-                for (int x = 0; x < W; ++x) M[n][k] = fmaxf(M[n][k], sh.m[x][c]);
-                const float f = ex2(a.m[n][k] - M[n][k]) * a.vmax;
+                for (int x = 0; x < W; ++x) M = fmaxf(M, sh.m[x][c]);
+#pragma unroll
+                for (int x = 0; x < W; ++x) Z = fmaxf(Z, sh.z[x][c] + (sh.m[x][c] - M));
+                const float f = ex2(sh.z[w][c] + (a.m[n][k] - M) - Z);
 #pragma unroll
                 for (int b = 0; b < 8; ++b) {
                     a.o[n][b][k] *= f;
@@ -877,10 +939,10 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
         const bool complete = cw.ja == 0 && cw.jb == cw.r.n;
         const uint64_t u0 = pre[cw.b] + (uint64_t)cw.row * cw.r.n;  // the row's first unit
         float* const parts = reinterpret_cast<float*>(p.ws + 64 + ATTN_MAX_CTAS);
-        auto store = [&](int c, float (&y)[4], float mx, float L) {
-            const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
+        auto store = [&](int c, float (&y)[4], float mx, float L, float Z) {  // Z: -126 .. 126
+            const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f, scale = ex2(Z);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] *= inv;
+            for (int e = 0; e < 4; ++e) y[e] = y[e] * inv * scale;
             if (p.rotate) rotate_warp(y, lane);
             const int j = (col0 + c) / p.group, hq_ = head * p.group + (col0 + c) - j * p.group;
             const int64_t row = cw.r.q0 + j;
@@ -893,11 +955,15 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
         // partial results: CTA c's slot 0 for a row that began before it, slot 1 for one that goes on after it
         float* const mine = parts + (size_t)(2 * blockIdx.x + (cw.ja == 0 ? 1 : 0)) * ATTN_PART;
         for (int c = w; c < tile_cols; c += W) {
-            float mx = ATTN_NONE, L = 0.0f, y[4] = {};
+            float mx = ATTN_NONE, Z = ATTN_NONE, L = 0.0f, y[4] = {};
 #pragma unroll
             for (int k = 0; k < W; ++k) mx = fmaxf(mx, sh.m[k][c]);
 #pragma unroll
-            for (int k = 0; k < W; ++k) L += ex2(sh.m[k][c] - mx) * sh.l[k][c];
+            for (int k = 0; k < W; ++k) {
+                const float d = sh.m[k][c] - mx;
+                L += ex2(d) * sh.l[k][c];
+                Z = fmaxf(Z, sh.z[k][c] + d);
+            }
 #pragma unroll
             for (int k = 0; k < W / 2; ++k) {
                 const float4 v = *reinterpret_cast<const float4*>(&sh.o[k][c][4 * lane]);
@@ -907,10 +973,10 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                 y[3] += v.w;
             }
             if (complete) {
-                store(c, y, mx, L);
+                store(c, y, mx, L, Z);
             } else {
                 __stcg(reinterpret_cast<float4*>(mine + c * 128 + 4 * lane), make_float4(y[0], y[1], y[2], y[3]));
-                if (lane == 0) __stcg(reinterpret_cast<float2*>(mine + ATTN_MAX_NC * 128 + 2 * c), make_float2(mx, L));
+                if (lane == 0) __stcg(reinterpret_cast<float4*>(mine + ATTN_MAX_NC * 128 + 4 * c), make_float4(mx, L, Z, 0.0f));
             }
         }
         if (!complete) {
@@ -925,14 +991,14 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
             }
             __syncthreads();
             if (sh.last) {
-                float mx[CPW], L[CPW], y[CPW][4];
+                float mx[CPW], L[CPW], Z[CPW], y[CPW][4];
 #pragma unroll
                 for (int x = 0; x < CPW; ++x) {
-                    mx[x] = ATTN_NONE;
+                    mx[x] = Z[x] = ATTN_NONE;
                     L[x] = y[x][0] = y[x][1] = y[x][2] = y[x][3] = 0.0f;
                 }
                 for (uint32_t k0 = first; k0 <= last; k0 += 4) {  // four results of the warp's columns on their way at a time
-                    float2 ml[CPW][4];
+                    float4 ml[CPW][4];
                     float4 v[CPW][4];
 #pragma unroll
                     for (int x = 0; x < CPW; ++x)
@@ -941,10 +1007,10 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                             const uint32_t k = k0 + z;
                             const int c = w + x * W;
                             const float* part = parts + (size_t)(2 * k + (k == first ? 1 : 0)) * ATTN_PART;
-                            ml[x][z] = make_float2(ATTN_NONE, 0.0f);
+                            ml[x][z] = make_float4(ATTN_NONE, 0.0f, ATTN_NONE, 0.0f);
                             v[x][z] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                             if (k <= last && c < tile_cols) {
-                                ml[x][z] = __ldcg(reinterpret_cast<const float2*>(part + ATTN_MAX_NC * 128 + 2 * c));
+                                ml[x][z] = __ldcg(reinterpret_cast<const float4*>(part + ATTN_MAX_NC * 128 + 4 * c));
                                 v[x][z] = __ldcg(reinterpret_cast<const float4*>(part + c * 128 + 4 * lane));
                             }
                         }
@@ -952,9 +1018,12 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                     for (int x = 0; x < CPW; ++x)
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
-                            const float t = fmaxf(mx[x], ml[x][z].x), fa = ex2(mx[x] - t), fb = ex2(ml[x][z].x - t);
+                            const float t = fmaxf(mx[x], ml[x][z].x), da = mx[x] - t, db = ml[x][z].x - t;
+                            const float za = Z[x] + da, zb = ml[x][z].z + db;
                             mx[x] = t;
-                            L[x] = L[x] * fa + ml[x][z].y * fb;
+                            L[x] = L[x] * ex2(da) + ml[x][z].y * ex2(db);
+                            Z[x] = fmaxf(za, zb);
+                            const float fa = ex2(za - Z[x]), fb = ex2(zb - Z[x]);
                             y[x][0] = y[x][0] * fa + v[x][z].x * fb;
                             y[x][1] = y[x][1] * fa + v[x][z].y * fb;
                             y[x][2] = y[x][2] * fa + v[x][z].z * fb;
@@ -963,7 +1032,7 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                 }
 #pragma unroll
                 for (int x = 0; x < CPW; ++x)
-                    if (w + x * W < tile_cols) store(w + x * W, y[x], mx[x], L[x]);
+                    if (w + x * W < tile_cols) store(w + x * W, y[x], mx[x], L[x], Z[x]);
             }
         }
         __syncthreads();  // the merge buffer, q and the piece's record are free again
