@@ -22,11 +22,11 @@
 // run one unit ahead, so warps never wait for one another inside a row; both
 // groups of a unit that every column sees go through one stretch of code.
 //
-// The running maximum moves only when a score exceeds it by 5 (in powers of
-// two), so the usual group needs no exchange between lanes: weights stay at
-// or below 32.  The decode scales of V are folded into them: what goes into FP16
-// is c = weight * decode scale, times a power of two per column that follows the
-// largest c of the tokens that the column sees (as the maximum does, 2^9 to 2^15),
+// The running maximum moves only when a lane's weights exceed 64, so the usual
+// group needs no exchange between lanes.  The decode scales of V are folded into
+// the weights: what goes into FP16 is c = weight * decode scale, times a power of
+// two per column that follows the largest c of the tokens that the column sees (as
+// the maximum does, 2^9 to 2^15),
 // never a token's scale alone: a large value without weight, outside the window, or
 // a vector of zeros (its decode scale is 1) leaves the others their bits.  A c is
 // good to 2^-11 down to 2^-23 of that largest one, to 2^-34 of it below.
@@ -416,112 +416,95 @@ __device__ __forceinline__ void attn_scores2(const uint8_t* unit, const uint4 (*
     }
 }
 
-// Moves the running maxima to scores s (N groups' worth).  The accumulators stay:
-// what their weights shrink by goes to the columns' powers of two.
-template <int NT, int N>
-__device__ __forceinline__ void attn_grow(AttnState<NT>& a, const float (&s)[N][NT][4]) {
-    bool grow = false;
-    float top[NT][2];
+// Weights of N groups (the first at `grp`) from their scores s and decode scales v
+// (of rows g, g + 8), as FP16 pairs u (FINE: their rest in lo) for the second
+// product; the weights are summed.  Where a lane's weights or contributions leave
+// their range, the running maxima go up to the scores, and the columns' powers of
+// two to where the largest contribution is 2^9 to 2^10.
+template <int NT, int N, bool FINE>
+__device__ __forceinline__ void attn_weigh(AttnState<NT>& a, const float (&s)[N][NT][4], float (&v)[N][2], const uint8_t* grp,
+                                           int lane, uint32_t (&u)[N][NT][2], uint32_t (&lo)[N][NT][2]) {
+    float sum[NT][2];
+    auto weigh = [&] {  // returns the largest of what goes into FP16
+        float most = 0.0f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            top[n][k] = fmaxf(s[0][n][k], s[0][n][2 + k]);
-#pragma unroll
-            for (int h = 1; h < N; ++h) top[n][k] = max3(top[n][k], s[h][n][k], s[h][n][2 + k]);
-            grow |= top[n][k] - a.m[n][k] > 5.0f;
-        }
-    if (!__any_sync(0xFFFFFFFFu, grow)) return;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            float t = top[n][k];
-#pragma unroll
-            for (int y = 4; y <= 16; y <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, y));
-            t = fmaxf(a.m[n][k], ceilf(t));
-            const float d = a.m[n][k] - t;
-            a.m[n][k] = t;
-            a.l[n][k] *= ex2(d);
-            // 2^-d more, as far as the range goes; the rest falls to the accumulators
-            const float e = (float)pow2_of(a.cz[n][k]) - d, z = fminf(e, 126.0f), f = ex2(z - e);
-            a.cz[n][k] = pow2((int)z);
-#pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                a.o[n][b][k] *= f;
-                a.o[n][b][2 + k] *= f;
+            for (int h = 0; h < N; ++h) {
+                const float e0 = ex2(s[h][n][0] - a.m[n][0]), e1 = ex2(s[h][n][1] - a.m[n][1]);
+                const float e2 = ex2(s[h][n][2] - a.m[n][0]), e3 = ex2(s[h][n][3] - a.m[n][1]);
+                sum[n][0] = h ? sum[n][0] + (e0 + e2) : e0 + e2;
+                sum[n][1] = h ? sum[n][1] + (e1 + e3) : e1 + e3;
+                const float w0 = e0 * v[h][0] * a.cz[n][0], w1 = e1 * v[h][0] * a.cz[n][1];
+                const float w2 = e2 * v[h][1] * a.cz[n][0], w3 = e3 * v[h][1] * a.cz[n][1];
+                most = max3(max3(most, w0, w1), w2, w3);
+                u[h][n][0] = pack_h2(w0, w1);
+                u[h][n][1] = pack_h2(w2, w3);
+                if constexpr (FINE) {
+                    const float2 a0 = h2f(u[h][n][0]), a1 = h2f(u[h][n][1]);
+                    lo[h][n][0] = pack_h2(w0 - a0.x, w1 - a0.y);
+                    lo[h][n][1] = pack_h2(w2 - a1.x, w3 - a1.y);
+                }
             }
-        }
-}
-
-// Scores s of N groups (the first at `grp`) become contributions, weight times
-// decode scale v (of rows g, g + 8), and the weights are summed.  The columns'
-// powers of two move down where a contribution would leave FP16's range, to
-// 2^9 .. 2^10 for the largest one.
-template <int NT, int N>
-__device__ __forceinline__ void attn_weigh(AttnState<NT>& a, float (&s)[N][NT][4], const float (&v)[N][2], const uint8_t* grp,
-                                           int lane) {
-    bool big = false;
-    float top[NT][2];
+        return most;
+    };
+    bool big = weigh() > 32768.0f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) big |= fmaxf(sum[n][0], sum[n][1]) > 64.0f;
+    if (__any_sync(0xFFFFFFFFu, big)) {
+        // vectors of zeros contribute nothing: all eight block scales of the token are zero
+        const int g = lane >> 2;
+#pragma unroll
+        for (int h = 0; h < N; ++h)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint4 f = *reinterpret_cast<const uint4*>(grp + h * KV_GROUP_BYTES + KV_V_SF + 64 * r + 16 * (g >> 1));
+                if (((f.x | f.y | f.z | f.w) & 0x00FF00FFu << 8 * (g & 1)) == 0) v[h][r] = 0.0f;
+            }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float t = fmaxf(s[0][n][k], s[0][n][2 + k]);
+#pragma unroll
+                for (int h = 1; h < N; ++h) t = max3(t, s[h][n][k], s[h][n][2 + k]);
+#pragma unroll
+                for (int y = 4; y <= 16; y <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, y));
+                t = fmaxf(a.m[n][k], ceilf(t));
+                const float d = a.m[n][k] - t;
+                a.m[n][k] = t;
+                a.l[n][k] *= ex2(d);
+                float c = 0.0f;
+#pragma unroll
+                for (int h = 0; h < N; ++h) c = max3(c, ex2(s[h][n][k] - t) * v[h][0], ex2(s[h][n][2 + k] - t) * v[h][1]);
+#pragma unroll
+                for (int y = 4; y <= 16; y <<= 1) c = fmaxf(c, __shfl_xor_sync(0xFFFFFFFFu, c, y));
+                // the accumulators' own power of two moves against the maximum (e), but not above 2^126 or to where the
+                // largest contribution leaves FP16's range; the rest falls to them
+                const float e = (float)pow2_of(a.cz[n][k]) - d, z = fminf(fminf(e, 126.0f), (float)(9 - pow2_of(c)));
+                const float f = ex2(z - e);
+                a.cz[n][k] = pow2((int)z);
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {
+                    a.o[n][b][k] *= f;
+                    a.o[n][b][2 + k] *= f;
+                }
+            }
+        weigh();
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int h = 0; h < N; ++h) {
-            const float e0 = ex2(s[h][n][0] - a.m[n][0]), e1 = ex2(s[h][n][1] - a.m[n][1]);
-            const float e2 = ex2(s[h][n][2] - a.m[n][0]), e3 = ex2(s[h][n][3] - a.m[n][1]);
-            a.l[n][0] += e0 + e2;
-            a.l[n][1] += e1 + e3;
-            s[h][n][0] = e0 * v[h][0];
-            s[h][n][1] = e1 * v[h][0];
-            s[h][n][2] = e2 * v[h][1];
-            s[h][n][3] = e3 * v[h][1];
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            top[n][k] = fmaxf(s[0][n][k], s[0][n][2 + k]);
-#pragma unroll
-            for (int h = 1; h < N; ++h) top[n][k] = max3(top[n][k], s[h][n][k], s[h][n][2 + k]);
-            big |= top[n][k] * a.cz[n][k] > 32768.0f;
-        }
+        a.l[n][0] += sum[n][0];
+        a.l[n][1] += sum[n][1];
     }
-    if (!__any_sync(0xFFFFFFFFu, big)) return;
-    // vectors of zeros contribute nothing: all eight block scales of the token are zero
-    const int g = lane >> 2;
-#pragma unroll
-    for (int h = 0; h < N; ++h)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const uint4 f = *reinterpret_cast<const uint4*>(grp + h * KV_GROUP_BYTES + KV_V_SF + 64 * r + 16 * (g >> 1));
-            if (((f.x | f.y | f.z | f.w) & 0x00FF00FFu << 8 * (g & 1)) == 0)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) s[h][n][2 * r] = s[h][n][2 * r + 1] = 0.0f;
-        }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            float t = fmaxf(s[0][n][k], s[0][n][2 + k]);
-#pragma unroll
-            for (int h = 1; h < N; ++h) t = max3(t, s[h][n][k], s[h][n][2 + k]);
-#pragma unroll
-            for (int y = 4; y <= 16; y <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, y));
-            const int e = pow2_of(a.cz[n][k]), z = min(e, 9 - pow2_of(t));  // (weights are at most 2^5, decode scales below 2^117)
-            const float f = ex2((float)(z - e));
-            a.cz[n][k] = pow2(z);
-#pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                a.o[n][b][k] *= f;
-                a.o[n][b][2 + k] *= f;
-            }
-        }
 }
 
-// Adds the group's weighted values.  s: contributions (attn_weigh); keep0, keep1:
+// Adds the group's weighted values.  u, lo: its weights (attn_weigh); keep0, keep1:
 // the bytes to keep of the block scales of the lane's tokens 2 i, 2 i + 1 and
 // 2 i + 8, + 9.
 template <int NT, bool MASK, bool FINE>
-__device__ __forceinline__ void attn_values(const uint8_t* grp, AttnState<NT>& a, const float (&s)[NT][4],
-                                            uint32_t keep0, uint32_t keep1, int lane) {
+__device__ __forceinline__ void attn_values(const uint8_t* grp, AttnState<NT>& a, const uint32_t (&u)[NT][2],
+                                            const uint32_t (&lo)[NT][2], uint32_t keep0, uint32_t keep1, int lane) {
     uint4 vf0 = *reinterpret_cast<const uint4*>(grp + KV_V_SF + (lane & 3) * 16);
     uint4 vf1 = *reinterpret_cast<const uint4*>(grp + KV_V_SF + (lane & 3) * 16 + 64);
     if constexpr (MASK) {
@@ -531,15 +514,11 @@ __device__ __forceinline__ void attn_values(const uint8_t* grp, AttnState<NT>& a
     uint32_t pb[NT][2], pl[NT][2];  // weights as the n side: column g, tokens 2 i, 2 i + 1 and 2 i + 8, + 9; FINE: their rest
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const float w0 = s[n][0] * a.cz[n][0], w1 = s[n][1] * a.cz[n][1];
-        const float w2 = s[n][2] * a.cz[n][0], w3 = s[n][3] * a.cz[n][1];
-        const uint32_t u = pack_h2(w0, w1), v2 = pack_h2(w2, w3);
-        pb[n][0] = transpose8x8(u);
-        pb[n][1] = transpose8x8(v2);
+        pb[n][0] = transpose8x8(u[n][0]);
+        pb[n][1] = transpose8x8(u[n][1]);
         if constexpr (FINE) {
-            const float2 a0 = h2f(u), a1 = h2f(v2);
-            pl[n][0] = transpose8x8(pack_h2(w0 - a0.x, w1 - a0.y));
-            pl[n][1] = transpose8x8(pack_h2(w2 - a1.x, w3 - a1.y));
+            pl[n][0] = transpose8x8(lo[n][0]);
+            pl[n][1] = transpose8x8(lo[n][1]);
         }
     }
     const uint4 c0 = *reinterpret_cast<const uint4*>(grp + KV_V_CODES + lane * 16);
@@ -834,10 +813,11 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                         v[h][0] = *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g);
                         v[h][1] = *reinterpret_cast<const float*>(grp + KV_V_DEC + 4 * g + 32);
                     }
-                    attn_grow<NT, 2>(a, s);
-                    attn_weigh<NT, 2>(a, s, v, unit, lane);
+                    uint32_t u[2][NT][2], lo[2][NT][2];
+                    attn_weigh<NT, 2, FINE>(a, s, v, unit, lane, u, lo);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) attn_values<NT, false, FINE>(unit + h * KV_GROUP_BYTES, a, s[h], 0u, 0u, lane);
+                    for (int h = 0; h < 2; ++h)
+                        attn_values<NT, false, FINE>(unit + h * KV_GROUP_BYTES, a, u[h], lo[h], 0u, 0u, lane);
                 } else if (t0 <= pos_max && !(p.window > 0 && t0 + 31 <= pos_min - p.window && t0 >= p.sinks)) {
                     // some do (in a chunk of a prefill, a unit may be ahead of all of these columns, or behind their window)
 #pragma unroll 1
@@ -861,9 +841,9 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                         const int e = pos_max - t1 - 2 * i4;  // the lane's even token is real if e >= 0, the odd one if e >= 1
                         const uint32_t keep0 = (e >= 0 ? 0x00FF00FFu : 0u) | (e >= 1 ? 0xFF00FF00u : 0u);
                         const uint32_t keep1 = (e >= 8 ? 0x00FF00FFu : 0u) | (e >= 9 ? 0xFF00FF00u : 0u);
-                        attn_grow<NT, 1>(a, s);
-                        attn_weigh<NT, 1>(a, s, v, grp, lane);
-                        attn_values<NT, true, FINE>(grp, a, s[0], keep0, keep1, lane);
+                        uint32_t u[1][NT][2], lo[1][NT][2];
+                        attn_weigh<NT, 1, FINE>(a, s, v, grp, lane, u, lo);
+                        attn_values<NT, true, FINE>(grp, a, u[0], lo[0], keep0, keep1, lane);
                     }
                 }
             }
