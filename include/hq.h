@@ -660,8 +660,9 @@ hq_status hq_kv4_gather(int dtype, const uint8_t *cache, int64_t num_pages, int 
  *  lse_opt    float [Tq, Hq] or NULL.
  *  Rows of out and lse behind the last request's are left as they were.
  *  ws         >= hq_kv4_attention_workspace_size() bytes, 16-byte aligned, in
- *             the rest state (hq_workspace_init); the call leaves it so.  Calls
- *             that share one must not overlap in time.
+ *             the rest state: the first HQ_KV4_ATTENTION_STATE_BYTES zero
+ *             (hq_workspace_init), the others may hold anything; the call leaves
+ *             it so.  Calls that share one must not overlap in time.
  * The workspace's error word (hq_get_error) is set to HQ_ERR_PAGE by a block-table
  * entry outside [0, num_pages) or a seq_len beyond the row's table_width *
  * page_size tokens (tokens without a page count as not seen), to HQ_ERR_SHAPE by a
@@ -682,6 +683,7 @@ hq_status hq_kv4_gather(int dtype, const uint8_t *cache, int64_t num_pages, int 
  *         HQ_ERR_UNSUPPORTED (dtype, hadamard_n, page_size, a negative window),
  *         HQ_ERR_CUDA.
  */
+#define HQ_KV4_ATTENTION_STATE_BYTES 2304
 size_t hq_kv4_attention_workspace_size(void);
 hq_status hq_kv4_attention(int dtype, const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t Tq,
                            int Hq, const uint8_t *cache, int64_t num_pages, int page_size, int Hkv,

@@ -1024,6 +1024,7 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
 // ------------------------------------------------------------------ launch
 // Words: [0..3] as the grouped call's workspace (only [2], the error word, is
 // used), [64 ..] arrivals per CTA, then two partial results per CTA.
+static_assert(4 * (64 + ATTN_MAX_CTAS) == HQ_KV4_ATTENTION_STATE_BYTES, "the words that are zero at rest");
 size_t attn_workspace_bytes() { return 4 * (64 + (size_t)ATTN_MAX_CTAS + 2 * (size_t)ATTN_MAX_CTAS * ATTN_PART); }
 
 template <int DT, int NT, int W, int MINB> static int launch_t(const AttnParams& p, int sms, cudaStream_t st) {

@@ -262,9 +262,9 @@ std::tuple<Tensor, Tensor> kv4_gather(const Tensor& cache, const Tensor& slots, 
 }
 
 // -------------------------------------------------------------- attention
-std::tuple<Tensor, Maybe> kv4_attention(const Tensor& q, const Tensor& cache, const Tensor& table, const Tensor& lens,
+std::tuple<Tensor, Maybe, Maybe> kv4_attention(const Tensor& q, const Tensor& cache, const Tensor& table, const Tensor& lens,
                                         const Maybe& cu_q, int q_len, std::optional<double> scale, int window, int sinks,
-                                        int hadamard_n, const Maybe& ws_in, const Maybe& out_in, bool want_lse) {
+                                        int hadamard_n, const Maybe& ws_in, const Maybe& out_in, bool want_lse, bool want_error) {
     const char* const what = "kv4_attention";
     const int dt = type_of(q.scalar_type());
     need(q.is_cuda() && (dt == HQ_DT_BF16 || dt == HQ_DT_F16) && is(cache, q, at::kByte) && is(table, q, at::kInt) &&
@@ -281,11 +281,11 @@ std::tuple<Tensor, Maybe> kv4_attention(const Tensor& q, const Tensor& cache, co
     const int64_t Tq = q.size(0), Hq = q.size(1);
     const On on(q);
     Tensor out = out_in ? *out_in : make({Tq, Hq, HQ_KV4_HEAD}, q, q.scalar_type());
-    Maybe lse, ws = ws_in;
+    Maybe lse, error, ws = ws_in;
     if (want_lse) lse = make({Tq, Hq}, q, at::kFloat);
     if (!ws) {
         ws = make({(int64_t)call.attention_ws()}, q, at::kByte);
-        const int s = call.ws_init(ws->data_ptr(), ws->nbytes(), on.stream);
+        const int s = call.ws_init(ws->data_ptr(), HQ_KV4_ATTENTION_STATE_BYTES, on.stream);
         need(s == HQ_OK, s, what);
     }
     const int s = call.attention(dt, q.data_ptr(), step(q, 0), step(q, 1), Tq, (int)Hq, static_cast<const uint8_t*>(cache.data_ptr()),
@@ -296,7 +296,11 @@ std::tuple<Tensor, Maybe> kv4_attention(const Tensor& q, const Tensor& cache, co
                                  out.data_ptr(), step(out, 0), step(out, 1), static_cast<float*>(ptr(lse)), ws->data_ptr(),
                                  ws->nbytes(), on.stream);
     need(s == HQ_OK, s, what);
-    return {out, lse};
+    if (want_error) {  // (a copy: the caller need not keep the workspace, nor does the next call change it)
+        error = make({1}, q, at::kInt);
+        error->copy_(at::from_blob(static_cast<char*>(ws->data_ptr()) + 8, {1}, error->options()));
+    }
+    return {out, lse, error};
 }
 
 }  // namespace

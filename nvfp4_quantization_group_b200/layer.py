@@ -23,6 +23,7 @@ HQ_NORM_MAX_K = 65536
 HQ_KV_MAX_REQUESTS = 4096
 HQ_KV_NO_PAGES, HQ_KV_NO_ROWS, HQ_KV_NO_WIDTH, HQ_KV_BAD_STATE = 1, 2, 4, 8
 HQ_KV4_HEAD, HQ_KV4_GROUP_TOKENS, HQ_KV4_GROUP_BYTES = 128, 16, 2432
+HQ_KV4_ATTENTION_STATE_BYTES = 2304
 
 _P, _I64, _SZ, _INT, _F, _D = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_float,
                                ctypes.c_double)
@@ -268,15 +269,23 @@ def kv4_attention_workspace(device="cuda", stream=None) -> torch.Tensor:
 def kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
                   cu_q: torch.Tensor | None = None, q_len: int = 1, scale: float | None = None, window: int = 0,
                   sinks: int = 0, hadamard_n: int = 128, ws: torch.Tensor | None = None, out: torch.Tensor | None = None,
-                  want_lse: bool = False, stream=None):
-    """Attention of q [Tq, Hq, 128], the newest tokens of each request, over the cache (see hq.h) -> out, or (out, lse
-    [Tq, Hq]) with want_lse.  Rows behind the last request's are left as they were (uninitialized in a new tensor).
-    scale: 1 / sqrt(128) unless given."""
+                  want_lse: bool = False, stream=None, want_error: bool = False):
+    """Attention of q [Tq, Hq, 128], the newest tokens of each request, over the cache (see hq.h) -> out; with want_lse
+    (out, lse [Tq, Hq]), with want_error also an int32 [1] on the device, last.  Rows behind the last request's are left
+    as they were (uninitialized in a new tensor).  scale: 1 / sqrt(128) unless given.
+
+    A page or length outside the cache, rows outside q and a wait that gave up are found on the device; the call returns
+    all the same, and what they concern counts as not seen or is not written.  They are reported by hq_get_error(ws), or
+    by want_error: the workspace's error word after the call (0: none).  Without either the report is lost: a call without
+    `ws` uses a workspace of its own (also slower: allocated and cleared each time)."""
     if stream is not None:
         return _on(stream, (q, cache, block_table, seq_lens, cu_q, ws, out), lambda: kv4_attention(
-            q, cache, block_table, seq_lens, cu_q, q_len, scale, window, sinks, hadamard_n, ws, out, want_lse))
-    o, lse = _x().kv4_attention(q, cache, block_table, seq_lens, cu_q, q_len, scale, window, sinks, hadamard_n, ws, out,
-                                want_lse)
+            q, cache, block_table, seq_lens, cu_q, q_len, scale, window, sinks, hadamard_n, ws, out, want_lse,
+            want_error=want_error))
+    o, lse, error = _x().kv4_attention(q, cache, block_table, seq_lens, cu_q, q_len, scale, window, sinks, hadamard_n, ws, out,
+                                       want_lse, want_error)
+    if want_error:
+        return (o, lse, error) if want_lse else (o, error)
     return (o, lse) if want_lse else o
 
 

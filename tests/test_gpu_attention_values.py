@@ -215,3 +215,58 @@ def test_a_score_far_above_the_others(hq, dtype, heads, rotate, std):
         part = 2.0 ** -11 if dtype == BF16 else 2.0 ** -22
         assert bool(((out.double() - want).abs() <= U[dtype] * want.abs() + (part + 2.0 ** -15) * size
                      + (2.0 ** -25 if dtype == F16 else 0.0) + rest * (128 ** 0.5 if rotate else 1)).all()), top
+
+
+# --------------------------------------------------------- calls without a workspace
+def _small(hq, g):
+    cache = hq.kv4_cache(8, 16, 2)
+    t = torch.arange(128, device="cuda")
+    hq.kv4_append(_normal(g, 128, 2, 128), _normal(g, 128, 2, 128), t, cache)
+    table = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+    return _normal(g, 2, 8, 128).to(BF16), cache, table, torch.tensor([64, 50], dtype=torch.int32, device="cuda")
+
+
+def test_errors_of_a_call_without_a_workspace(hq):
+    """The device's report comes back with want_error, with a workspace or without, captured or not."""
+    q, cache, table, lens = _small(hq, _gen(1800))
+    want = hq.kv4_attention(q, cache, table, lens)
+    ws, side = hq.kv4_attention_workspace(), torch.cuda.Stream()
+    bad = table.clone()
+    bad[1, 2] = 8
+    cu = torch.tensor([0, 1, 9], dtype=torch.int32, device="cuda")
+    for kw in ({}, {"ws": ws}, {"stream": side}):
+        for args, status in (({}, 0), ({"block_table": bad}, hq.HQ_ERR_PAGE), ({"cu_q": cu}, hq.HQ_ERR_SHAPE), ({}, 0)):
+            torch.cuda.synchronize()
+            o, lse, error = hq.kv4_attention(**{"q": q, "cache": cache, "block_table": table, "seq_lens": lens, **args}, **kw,
+                                             want_lse=True, want_error=True)
+            torch.cuda.synchronize()
+            assert error.dtype == torch.int32 and error.tolist() == [status]
+            assert torch.equal(o[0], want[0]) and lse.shape == (2, 8)
+            if "ws" in kw:
+                assert hq.hq_get_error(ws) == status
+    o, error = hq.kv4_attention(q, cache, table, lens, want_error=True)
+    assert torch.equal(o, want) and int(error) == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, error = hq.kv4_attention(q, cache, table, lens, want_error=True)
+    for entry, status in ((8, hq.HQ_ERR_PAGE), (6, 0), (-1, hq.HQ_ERR_PAGE)):
+        table[1, 2] = entry
+        graph.replay()
+        assert int(error) == status and torch.equal(o[0], want[0])
+
+
+def test_a_workspace_of_the_calls_own_from_used_memory(hq):
+    q, cache, table, lens = _small(hq, _gen(1900))
+    ws = hq.kv4_attention_workspace()
+    want = hq.kv4_attention(q, cache, table, lens, ws=ws)
+    for byte in (0xFF, 0x01, 0x7F):
+        used = torch.full((hq.hq_kv4_attention_workspace_size(),), byte, dtype=torch.uint8, device="cuda")
+        del used
+        o, error = hq.kv4_attention(q, cache, table, lens, want_error=True)
+        assert torch.equal(o, want) and int(error) == 0
+    # of a workspace only the stated part has to be zero
+    ws.fill_(0xFF)
+    ws[:hq.HQ_KV4_ATTENTION_STATE_BYTES] = 0
+    for _ in range(2):
+        assert torch.equal(hq.kv4_attention(q, cache, table, lens, ws=ws), want)
+    assert hq.hq_get_error(ws) == 0
