@@ -7,6 +7,7 @@
 // The C functions are reached through the addresses that bind() is given (the
 // library that the package has loaded); refusals become the package's HQError.
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -90,6 +91,13 @@ inline Tensor part(const Tensor& t, int64_t at, at::IntArrayRef shape) {
     return r;
 }
 
+// These calls record no gradients: an input that wants one while autograd records would lose it unseen.
+inline bool tracked(const Tensor& t) { return t.requires_grad(); }
+inline bool tracked(const Maybe& t) { return t && t->requires_grad(); }
+template <typename... T> inline void untracked(const char* what, const T&... t) {
+    need(!(at::GradMode::is_enabled() && (tracked(t) || ...)), HQ_ERR_UNSUPPORTED, what);
+}
+
 // Makes the tensors' device current and gives its current stream.
 struct On {
     c10::cuda::CUDAGuard guard;
@@ -104,6 +112,8 @@ std::tuple<Tensor, Tensor, Maybe, Maybe, Maybe> add_rmsnorm(const Tensor& x, con
                                                             bool want_rstd, bool want_amax, const Maybe& residual_out) {
     const char* const what = "add_rmsnorm_fp8_k128";
     const int dt = type_of(x.scalar_type()), wt = type_of(weight.scalar_type());
+    untracked("add_rmsnorm_fp8_k128 records no gradients: call it under torch.no_grad() (they are rmsnorm_backward's)", x, weight,
+              residual, residual_out);
     need(x.is_cuda() && dt >= 0 && weight.device() == x.device() && (wt == dt || wt == HQ_DT_F32) && fits(residual, x) &&
              fits(residual_out, x),
          HQ_ERR_UNSUPPORTED, "add_rmsnorm_fp8_k128: tensors of one CUDA device and type (the weight may be FP32) are needed");
@@ -137,6 +147,7 @@ std::tuple<Tensor, Maybe> rmsnorm_backward(const Tensor& dy, const Tensor& h, co
                                            const Maybe& dres, bool want_dweight, const Maybe& ws_in, const Maybe& dx_in) {
     const char* const what = "rmsnorm_backward";
     const int dt = type_of(dy.scalar_type()), wt = type_of(weight.scalar_type());
+    untracked("rmsnorm_backward records no gradients of its own: call it under torch.no_grad()", dy, h, dres, dx_in);
     need(dy.is_cuda() && dt >= 0 && fits(h, dy) && weight.device() == dy.device() && (wt == dt || wt == HQ_DT_F32) &&
              is(rstd, dy, at::kFloat) && fits(dres, dy) && fits(dx_in, dy) && (!ws_in || ws_in->device() == dy.device()),
          HQ_ERR_UNSUPPORTED, "rmsnorm_backward: tensors of one CUDA device and type (weight and rstd FP32) are needed");
@@ -168,6 +179,7 @@ std::tuple<Tensor, Maybe> rope(const Tensor& q, const Maybe& k, const Tensor& po
                                int layout, double magnitude, bool inverse, const Maybe& q_out, const Maybe& k_out) {
     const char* const what = "rope";
     const int dt = type_of(q.scalar_type());
+    untracked("rope records no gradients: call it under torch.no_grad() (they are rope's with inverse)", q, k, q_out, k_out);
     need(q.is_cuda() && dt >= 0 && fits(k, q) && is(positions, q, at::kLong) && is(inv_freq, q, at::kDouble) && fits(q_out, q) &&
              fits(k_out, q),
          HQ_ERR_UNSUPPORTED, "rope: tensors of one CUDA device and type, int64 positions, float64 inv_freq are needed");
@@ -227,6 +239,7 @@ inline int cache_page(const Tensor& c) { return (int)std::min<int64_t>(c.size(2)
 void kv4_append(const Tensor& k, const Tensor& v, const Tensor& slots, const Tensor& cache, int hadamard_n) {
     const char* const what = "kv4_append";
     const int dt = type_of(k.scalar_type());
+    untracked("kv4_append records no gradients: call it under torch.no_grad()", k, v);
     need(cache.is_cuda() && cache.scalar_type() == at::kByte && k.device() == cache.device() && dt >= 0 && fits(v, k) &&
              is(slots, k, at::kLong),
          HQ_ERR_UNSUPPORTED, "kv4_append: k and v of one type, int64 slots and a uint8 cache on one CUDA device are needed");
@@ -267,6 +280,7 @@ std::tuple<Tensor, Maybe, Maybe> kv4_attention(const Tensor& q, const Tensor& ca
                                         int hadamard_n, const Maybe& ws_in, const Maybe& out_in, bool want_lse, bool want_error) {
     const char* const what = "kv4_attention";
     const int dt = type_of(q.scalar_type());
+    untracked("kv4_attention records no gradients: call it under torch.no_grad()", q, out_in);
     need(q.is_cuda() && (dt == HQ_DT_BF16 || dt == HQ_DT_F16) && is(cache, q, at::kByte) && is(table, q, at::kInt) &&
              is(lens, q, at::kInt) && is(cu_q, q, at::kInt) && fits(out_in, q) && (!ws_in || ws_in->device() == q.device()),
          HQ_ERR_UNSUPPORTED, "kv4_attention: BF16 or FP16 q and out, a uint8 cache, int32 tables on one CUDA device are needed");

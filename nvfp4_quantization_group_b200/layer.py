@@ -7,6 +7,10 @@ tokens is bound by the host's part of a call).  Tensors may lie on any CUDA devi
 work goes to that device's current stream, or to `stream`.  With `stream` the outputs are allocated on it and the inputs
 recorded on it, so that they may be dropped as soon as the call returns.  A refused call raises HQError, as in the rest
 of the package.
+
+None of them records gradients.  Rows that require a gradient (and the norm's weight) are refused while autograd records,
+so that none is lost unseen: call them under torch.no_grad() or inside an autograd.Function, whose backward pass is
+rmsnorm_backward or rope(..., inverse=True).
 """
 from __future__ import annotations
 
