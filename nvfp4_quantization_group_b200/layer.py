@@ -104,7 +104,7 @@ def add_rmsnorm_fp8_k128(x: torch.Tensor, weight: torch.Tensor, residual: torch.
                          want_amax: bool = False, residual_out: torch.Tensor | None = None, stream=None) -> dict:
     """Residual addition, RMS norm and K128 FP8 codes of [M, K] rows (see hq.h) -> dict with codes [M, K], scales,
     residual_out (with a residual: what the norm read; into `residual_out` where given, which may be x or residual
-    itself) and, when asked, rstd [M] and amax (they share the scales' allocation)."""
+    itself) and, when asked, rstd [M] and amax (up to 32 KB of scales share an allocation with them)."""
     if stream is not None:
         return _on(stream, (x, weight, residual, residual_out), lambda: add_rmsnorm_fp8_k128(
             x, weight, residual, eps, scale_layout, scale_ld, want_rstd, want_amax, residual_out))
