@@ -8,10 +8,12 @@ layer.py on torch tensors, which call those entry points.
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -51,20 +53,32 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build_torch(force: bool = False) -> str:
-    """Compile the torch-tensor conveniences (when their source changed) and return their path."""
-    deps = [TORCH_SRC, os.path.join(INCLUDE, "hq.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(TORCH_LIB) and all(os.path.getmtime(d) <= os.path.getmtime(TORCH_LIB) for d in deps):
-        return TORCH_LIB
-    import sysconfig
+def built_for() -> str:
+    """What the conveniences' binary interface depends on; compiled into them."""
+    return f"hq_torch for torch {importlib.metadata.version('torch')}, {sysconfig.get_config_var('SOABI')}"
 
+
+def torch_lib_fits() -> bool:
+    """Whether the conveniences on disk were compiled for this torch and Python (loading others may crash)."""
+    try:
+        with open(TORCH_LIB, "rb") as f:
+            return built_for().encode() + b"\0" in f.read()
+    except FileNotFoundError:
+        return False
+
+
+def build_torch(force: bool = False) -> str:
+    """Compile the torch-tensor conveniences (when their source, torch or Python changed) and return their path."""
+    deps = [TORCH_SRC, os.path.join(INCLUDE, "hq.h"), os.path.abspath(__file__)]
+    if not force and torch_lib_fits() and all(os.path.getmtime(d) <= os.path.getmtime(TORCH_LIB) for d in deps):
+        return TORCH_LIB
     import torch
     from torch.utils.cpp_extension import include_paths
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     include = [*include_paths(), os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
     tmp = TORCH_LIB + f".{os.getpid()}.tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(x for i in include for x in ("-I", i)),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DHQ_BUILT_FOR="{built_for()}"', *(x for i in include for x in ("-I", i)),
            TORCH_SRC, "-o", tmp, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-lc10_cuda", "-ltorch",
            "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -337,6 +337,7 @@ PYBIND11_MODULE(_hq_torch, m) {
     });
     // (the allocator may wait for the device: other Python threads run meanwhile)
     const py::call_guard<py::gil_scoped_release> free;
+    m.attr("built_for") = HQ_BUILT_FOR;  // (the build looks for it in the file)
     m.def("bind", &bind);
     m.def("add_rmsnorm", &add_rmsnorm, free);
     m.def("rmsnorm_backward", &rmsnorm_backward, free);

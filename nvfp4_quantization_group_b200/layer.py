@@ -57,6 +57,10 @@ def _x():
     """The compiled conveniences, bound to the loaded library (raises if they have not been built: there is no fallback)."""
     global _torch_calls
     if _torch_calls is None:
+        from . import _build
+        if not _build.torch_lib_fits():
+            raise OSError(f"{_build.TORCH_LIB} is missing or was built for another torch or Python: run "
+                          "nvfp4_quantization_group_b200/_build.py")
         from . import _hq_torch
         L = lib()
         _hq_torch.bind({n: ctypes.cast(getattr(L, n), _P).value for n in (*SIGNATURES, "hq_workspace_init")})
