@@ -177,12 +177,19 @@ def measured_peaks() -> dict:
         return {"hbm_gbs": FALLBACK_HBM_GBS, "source": "fallback"}
 
 
-def kernel_source_sha() -> str:
-    """Hash of the CUDA sources: ncu traffic figures are only valid for the
+def kernel_sources(workload: str) -> list[str]:
+    """The sources that a workload's launches come from: its kernels, what they include, and the entry points that size
+    their grids."""
+    kernels = "hq_nvfp4.cu" if workload.startswith(("grouped_", "dense_")) else "hq_fp8.cu"
+    return sorted((kernels, "hq_api.cu", "hq_device.cuh", "hq_internal.h"))
+
+
+def kernel_source_sha(workload: str, csrc: str | None = None) -> str:
+    """Hash of a workload's sources: ncu traffic figures are only valid for the
     kernels they were captured on."""
     h = hashlib.sha256()
-    csrc = os.path.join(ROOT, "nvfp4_quantization_group_b200", "csrc")
-    for name in sorted(os.listdir(csrc)):
+    csrc = csrc or os.path.join(ROOT, "nvfp4_quantization_group_b200", "csrc")
+    for name in kernel_sources(workload):
         with open(os.path.join(csrc, name), "rb") as f:
             h.update(name.encode())
             h.update(f.read())
@@ -193,7 +200,7 @@ def recorded_traffic(workload: str):
     """DRAM bytes per launch from profiles/traffic.txt ("workload sha bytes"),
     or None when missing or captured on other kernel sources."""
     path = os.path.join(ROOT, "profiles", "traffic.txt")
-    sha = kernel_source_sha()
+    sha = kernel_source_sha(workload)
     try:
         for line in open(path):
             parts = line.split()
