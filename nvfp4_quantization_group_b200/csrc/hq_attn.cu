@@ -15,7 +15,7 @@
 // (hi + lo, 22 bits), so scores are FP32-like.  The weights P are rounded to FP16
 // once for BF16 outputs, whose own rounding is eight times as coarse; for FP16
 // outputs they too go in two parts (the error against 64 bits is then the output's
-// own, 2.1e-4, where one part gives 2.9e-4; 114 -> 123 us at the sizes below).
+// own, 2.1e-4, where one part gives 2.9e-4; 117 -> 122 us at the sizes below).
 // The cache's byte order gives each lane its operands of a group as 16-byte
 // pieces (four for the codes, three for the block scales).  A warp takes one
 // or two groups (a unit) at a time, copied into its own ring by bulk copies that
@@ -34,10 +34,13 @@
 // Bound: the codes and scales are 152 bytes per token and key/value head, but a
 // group also costs about 370 warp instructions, 64 of them conversions of code
 // pairs at half rate.  32 requests of 8000 to 16384 tokens, 64 query and 8
-// key/value heads: 114 us, 4.2 TB/s (64 % of the measured copy rate); issue slots
-// 59 % busy, ALU 53 %, matrix 31 %, no more than four warps a scheduler to fill the
-// gaps (128 registers each; 96 would spill).  Steps there: one group a turn 166,
-// two 133, look-ups by whole lanes 121, both groups' scores together 116.  (These
+// key/value heads: 117 us replayed 30 times, 4.1 TB/s (63 % of the measured copy
+// rate), 126 to 128 us called for a second.  Nothing is full (issue slots 58 % busy,
+// ALU 52 %, matrix 30 %): what limits it now is latency at four warps a scheduler
+// (128 registers each, 40 bytes of them spilled; 96 would spill more).  Steps there:
+// one group a turn 166, two 133, look-ups by whole lanes 121, both groups' scores
+// together 114, contributions in place of decode scales 118, their range checked
+// once a unit 117.  (These
 // matrix instructions, not tcgen05: that one reads its operands from shared memory,
 // where K and V would have to be widened first: 512 bytes per token and head
 // written and read again, 8 clocks of an SM's shared memory beside the 2.4 of the
@@ -265,7 +268,8 @@ template <int NT, int W> struct AttnShared {
         float4 frag[W / 2][NT * 8][32];   // accumulators of the upper half's warps
         float o[W / 2][NC][OS];           // results of the lower half's warps
     };
-    float m[W][NC], l[W][NC], z[W][NC];
+    float2 mz[W][NC];  // a warp's maximum and power of two of each column
+    float l[W][NC];
     float qs[NC];  // factor of a column's scores, in powers of two
     int pos[NC];   // a column's position
     Walk cw, nw;   // the CTA's current piece and the one after it
@@ -860,9 +864,8 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
 #pragma unroll
                 for (int x = 4; x <= 16; x <<= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, x);
                 if (g == 0) {
-                    sh.m[w][8 * n + 2 * i4 + k] = a.m[n][k];
+                    sh.mz[w][8 * n + 2 * i4 + k] = make_float2(a.m[n][k], (float)-pow2_of(a.cz[n][k]));
                     sh.l[w][8 * n + 2 * i4 + k] = t;
-                    sh.z[w][8 * n + 2 * i4 + k] = (float)-pow2_of(a.cz[n][k]);
                 }
             }
         __syncthreads();
@@ -875,10 +878,10 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                 const int c = 8 * n + 2 * i4 + k;
                 float M = ATTN_NONE, Z = ATTN_NONE;
 #pragma unroll
-                for (int x = 0; x < W; ++x) M = fmaxf(M, sh.m[x][c]);
+                for (int x = 0; x < W; ++x) M = fmaxf(M, sh.mz[x][c].x);
 #pragma unroll
-                for (int x = 0; x < W; ++x) Z = fmaxf(Z, sh.z[x][c] + (sh.m[x][c] - M));
-                const float f = ex2(sh.z[w][c] + (a.m[n][k] - M) - Z);
+                for (int x = 0; x < W; ++x) Z = fmaxf(Z, sh.mz[x][c].y + (sh.mz[x][c].x - M));
+                const float f = ex2((float)-pow2_of(a.cz[n][k]) + (a.m[n][k] - M) - Z);
 #pragma unroll
                 for (int b = 0; b < 8; ++b) {
                     a.o[n][b][k] *= f;
@@ -937,12 +940,13 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
         for (int c = w; c < tile_cols; c += W) {
             float mx = ATTN_NONE, Z = ATTN_NONE, L = 0.0f, y[4] = {};
 #pragma unroll
-            for (int k = 0; k < W; ++k) mx = fmaxf(mx, sh.m[k][c]);
+            for (int k = 0; k < W; ++k) mx = fmaxf(mx, sh.mz[k][c].x);
 #pragma unroll
             for (int k = 0; k < W; ++k) {
-                const float d = sh.m[k][c] - mx;
+                const float2 v = sh.mz[k][c];
+                const float d = v.x - mx;
                 L += ex2(d) * sh.l[k][c];
-                Z = fmaxf(Z, sh.z[k][c] + d);
+                Z = fmaxf(Z, v.y + d);
             }
 #pragma unroll
             for (int k = 0; k < W / 2; ++k) {
@@ -995,20 +999,30 @@ __global__ void __launch_bounds__(32 * W, MINB) kv4_attention_kernel(AttnParams 
                             }
                         }
 #pragma unroll
-                    for (int x = 0; x < CPW; ++x)
+                    for (int x = 0; x < CPW; ++x) {
+                        float t = mx[x];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) t = fmaxf(t, ml[x][z].x);
+                        const float za = Z[x] + (mx[x] - t);
+                        float zt = za;
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) zt = fmaxf(zt, ml[x][z].z + (ml[x][z].x - t));
+                        const float fa = ex2(za - zt);
+                        L[x] *= ex2(mx[x] - t);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[x][e] *= fa;
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
-                            const float t = fmaxf(mx[x], ml[x][z].x), da = mx[x] - t, db = ml[x][z].x - t;
-                            const float za = Z[x] + da, zb = ml[x][z].z + db;
-                            mx[x] = t;
-                            L[x] = L[x] * ex2(da) + ml[x][z].y * ex2(db);
-                            Z[x] = fmaxf(za, zb);
-                            const float fa = ex2(za - Z[x]), fb = ex2(zb - Z[x]);
-                            y[x][0] = y[x][0] * fa + v[x][z].x * fb;
-                            y[x][1] = y[x][1] * fa + v[x][z].y * fb;
-                            y[x][2] = y[x][2] * fa + v[x][z].z * fb;
-                            y[x][3] = y[x][3] * fa + v[x][z].w * fb;
+                            const float d = ml[x][z].x - t, fb = ex2(ml[x][z].z + d - zt);
+                            L[x] += ml[x][z].y * ex2(d);
+                            y[x][0] += v[x][z].x * fb;
+                            y[x][1] += v[x][z].y * fb;
+                            y[x][2] += v[x][z].z * fb;
+                            y[x][3] += v[x][z].w * fb;
                         }
+                        mx[x] = t;
+                        Z[x] = zt;
+                    }
                 }
 #pragma unroll
                 for (int x = 0; x < CPW; ++x)
@@ -1044,7 +1058,8 @@ int launch_attn(int dtype, const AttnParams& p, int sms, cudaStream_t st) {
     // against 12), so they are paired when their number is even.  (Up to 20
     // columns, three tiles, of 48 verifying requests: 44 us paired, half a pass
     // empty, against 38.)  Six warps a block, as one of eight with 255 registers
-    // or two blocks of four take 172 and 167 us there.
+    // or two blocks of four take 172 and 167 us there.  (As measured when chosen;
+    // 163 us there now.  168 registers spill about 200 bytes a thread.)
     const bool wide = ((int64_t)p.q_len * p.group + 7) / 8 % 2 == 0;
     if (dtype == HQ_DT_BF16)
         return wide ? launch_t<HQ_DT_BF16, 2, 6, 2>(p, sms, st) : launch_t<HQ_DT_BF16, 1, 8, 2>(p, sms, st);
