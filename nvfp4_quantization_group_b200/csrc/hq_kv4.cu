@@ -177,10 +177,14 @@ void launch_slots(const SlotParams& p, int sms, cudaStream_t st) {
 // vectors and, on the side of the cache, elements 16 b + 4 i .. + 3 of every
 // block b (i the thread of the four): the 16 bytes of keys' codes, or two times
 // 8 bytes of values' codes, that lie together in a group.  The tokens of a tile
-// usually fill one group, whose sectors are then written whole.  Bound by the
-// instructions (issue slots 70 % busy in append, 57 % in gather): butterflies, exact
-// quotients, conversions.  16384 tokens x 8 heads written and read back: 46 us, 3.8
-// TB/s.
+// usually fill one group, whose sectors are then written whole.  Append is bound by
+// its instructions (issue slots 70 % busy): butterflies, exact quotients, conversions.
+// Gather is not (57 %, 66 % of the copy rate as stored): with one tile in flight and a
+// third of an SM's warps it waits for its loads.  16384 tokens x 8 heads in BF16: append
+// 27 us (21 without the rotation), gather 24 rotated back and 20 as stored, where the
+// bytes need 13.5 each; in FP32 42 (152 bytes spilled under the cap below), 40, 40 and
+// 39 for 24.  Times are of twenty to thirty replays; append and gather called for a
+// second take 49 us where they take 46 replayed.
 constexpr int KV_THREADS = 128;
 // Resident blocks that the registers are capped for: 16384 tokens x 8 heads
 // written and read back take 46 us with 6, 48 uncapped (4 to 5), 54 with 5 or 7,

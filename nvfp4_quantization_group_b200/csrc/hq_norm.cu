@@ -5,9 +5,13 @@
 // y = (h rstd) w, then the K128 FP8 rule.  Backward, per row: g = dy w,
 // c = rstd^2 mean(g h), dx = rstd (g - h c) + dres, and over the rows
 // dw = sum dy h rstd.  A handful of operations per element: bound by the bytes.
-// Every input byte is read once and every output byte written once: a row stays
-// in registers between its sum and its second use, and the loads of a thread's
-// next row are in flight meanwhile.
+// Up to K = 8192 every input byte is read once and every output byte written once: a
+// row stays in registers between its sum and its second use, and the loads of a
+// thread's next row are in flight meanwhile.  Longer rows are held too, but nothing is
+// loaded ahead and part of them spills (forward 220 to 1472 bytes a thread; the
+// gradients up to 352 at 16384, 1.7 to 2.6 KB beyond), and beyond 16384 the gradients
+// read dy and h twice.  Times are of thirty replays; called for a second the largest
+// cases take 5 to 15 % more (the clocks go down).
 #include "hq_layer.cuh"
 
 namespace hq {
@@ -123,8 +127,10 @@ static void norm_launch(const NormParams& p, int threads, int sms, cudaStream_t 
 // Who holds a row.  Few rows: one chunk a thread, for the shortest chain.  Many:
 // two chunks a thread with two blocks of 512 threads an SM, so that 57 KB of the
 // next rows are in flight on each while one is worked on ([16384, 7168] BF16 with
-// a residual: 147 us, 5.6 TB/s; four chunks in blocks of 256 179 us, without the
-// loads ahead 196 us, one chunk in blocks of 1024 204 us).
+// a residual: 148 us, 5.6 TB/s; four chunks in blocks of 256 179 us, without the
+// loads ahead 196 us, one chunk in blocks of 1024 204 us).  An FP32 weight leaves
+// room for one block an SM: 273 us there; FP32 rows [8192, 7168] 170 us for 118 of
+// copying.  [8192, 16384] BF16 255 us for 146, FP32 [4096, 16384] 302 for 135.
 template <int DT, int WDT> static void norm_t(const NormParams& p, int sms, cudaStream_t st) {
     constexpr int TWO = DT == HQ_DT_F32 || WDT == HQ_DT_F32 ? 1 : 2;  // (FP32 chunks need the registers of both)
     const int chunks = (int)(p.K / 8);
@@ -309,7 +315,9 @@ static int norm_back_launch(const NormBackParams& p, int threads, int sms, cudaS
     return grid;
 }
 // Two chunks a thread and two blocks of 512 threads an SM ([8191, 4096] BF16 with
-// dres: 52 us, 5.2 TB/s; one block an SM 61 us, four chunks a thread 54 us, one 72 us).
+// dres: 52 us, 5.2 TB/s; one block an SM 61 us, four chunks a thread 54 us, one 72 us;
+// FP32 100 us for 83 of copying).  [4096, 16384] 104 us for 83 in BF16, 307 for 166 in
+// FP32; [2048, 32768] BF16 582 for 83.
 template <int DT, int WDT> static void norm_back_t(const NormBackParams& p, int sms, cudaStream_t st) {
     constexpr int TWO = DT == HQ_DT_F32 || WDT == HQ_DT_F32 ? 1 : 2;
     const int chunks = (int)(p.K / 8);
