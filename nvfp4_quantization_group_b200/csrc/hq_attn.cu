@@ -26,10 +26,10 @@
 // group needs no exchange between lanes.  The decode scales of V are folded into
 // the weights: what goes into FP16 is c = weight * decode scale, times a power of
 // two per column that follows the largest c of the tokens that the column sees (as
-// the maximum does, 2^9 to 2^15),
-// never a token's scale alone: a large value without weight, outside the window, or
-// a vector of zeros (its decode scale is 1) leaves the others their bits.  A c is
-// good to 2^-11 down to 2^-23 of that largest one, to 2^-34 of it below.
+// the maximum does, 2^9 to 2^15), never a token's scale alone: a large value without
+// weight, outside the window, or a vector of zeros (its decode scale is 1) leaves the
+// others their bits.  A c is good to 2^-11 down to 2^-23 of that largest one, to
+// 2^-34 of it below.
 //
 // Bound: the codes and scales are 152 bytes per token and key/value head, but a
 // group also costs about 370 warp instructions, 64 of them conversions of code
